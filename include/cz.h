@@ -315,6 +315,122 @@ int cz_profile_read(double* ms, int64_t* launches, int32_t n_kinds);
  * context stays usable.  Returns CZ_OK when enqueued. */
 int cz_selftest_bounded_wait(int64_t timeout_ns, void* workspace, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a training step around the Muon step: 8-bit activation
+ * checkpoints and the weight gradient taken from them, the norms around a block
+ * with its gate and residual scale, and token log probabilities.  The pages have
+ * no counterpart; they produce the gradients that the flat buffer holds.
+ *
+ * Common to all: matrices are row-major with rows `ld` elements apart (ld >= the
+ * row's length) and a pointer aligned to its element; any alignment and stride is
+ * taken, rows that start on 16-byte boundaries are fastest.  Outputs do not overlap
+ * inputs unless the call says so.  Calls are asynchronous on `stream`, allocate
+ * nothing, keep nothing between calls and can be captured in a CUDA graph.
+ * Results are bit for bit the same from call to call.  Zero rows is a valid size.
+ * Invalid arguments give CZ_ERR_INVALID before anything is enqueued; a device
+ * other than sm_103 gives CZ_ERR_UNSUPPORTED. */
+#define CZ_BF16 0
+#define CZ_F32  1
+
+/* Checkpoint of a rows x cols activation: blocks of 32 columns of a row hold signed
+ * 8-bit q and share a power of two: x^ = q * 2^E, E the smallest integer >= -126 with
+ * max|x| <= 127 * 2^E, q = x / 2^E rounded to nearest even: |x^ - x| <= max|x| / 127.
+ * x^ is exact in bf16 and fp32.  A block with an infinity or a NaN reads back as
+ * NaN.  cz_act_size gives the buffer's bytes; the buffer is 16-byte aligned device
+ * memory and needs no initialisation.  Layout: rows of round_up(cols, 32) q bytes
+ * (zeros past cols), then, from the next multiple of 128 bytes, rows of
+ * round_up(round_up(cols, 32) / 32, 16) bytes E + 127 (255: not finite). */
+int cz_act_size(int64_t rows, int64_t cols, size_t* bytes);
+/* x (dtype CZ_BF16 or CZ_F32, stride ld) -> ckpt. */
+int cz_act_encode(const void* x, int32_t dtype, int64_t ld, int64_t rows, int64_t cols, void* ckpt, void* stream);
+/* ckpt -> x, for recomputing a block from its kept input. */
+int cz_act_decode(const void* ckpt, int64_t rows, int64_t cols, void* x, int32_t dtype, int64_t ld, void* stream);
+
+/* Weight gradient of a linear layer from the checkpoint of its input:
+ *   out[n_out x n_in] = add + sum over rows of dy[row, :]^T x^[row, :]
+ * dy: bf16 rows x n_out, stride ld_dy.  ckpt: cz_act_* checkpoint of rows x n_in.
+ * out: out_dtype, dense rows of n_in elements (a tensor of the flat gradient buffer,
+ * fp32 or bf16, as the Muon step reads it); add: nullable, the same type and layout
+ * (add == out accumulates in place).  Sums are fp32, out is rounded once.
+ * workspace: >= cz_act_wgrad_workspace bytes, 256-byte aligned; its first 256 bytes
+ * (the status word) must be zero before first use; cz_device_status(stream,
+ * workspace) reads it.  Concurrent calls need workspaces of their own. */
+int cz_act_wgrad_workspace(const void* dy, int64_t ld_dy, int64_t rows, int64_t n_out, int64_t n_in, size_t* bytes);
+int cz_act_wgrad(const void* dy, int64_t ld_dy, const void* ckpt, int64_t rows, int64_t n_out, int64_t n_in,
+                 const void* add, void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The norms before and after a block, with its gate and the residual scales.
+ * Forward, a row at a time (h: the residual stream, y: the block's output):
+ *   n  = y r_y w_post,  r_y = (mean y^2 + eps)^-1/2     (n = y when post_norm = 0)
+ *   h' = h_scale h + y_scale act(gate) n                (act(gate) = 1 without a gate)
+ *   x  = h' r_h w_pre,  r_h = (mean h'^2 + eps)^-1/2    (the next block's input)
+ * Backward: the gradients of h, y, the weights and the gate from those of h' (dh_in)
+ * and x (dx); it needs h', y, r_y and r_h of the forward, h' and y as tensors or as
+ * checkpoints.  Sums are fp32. */
+#define CZ_NORM_MAX_COLS 16384
+#define CZ_GATE_NONE    0   /* gate kinds */
+#define CZ_GATE_CHANNEL 1   /* fp32, one value a column, shared by all rows */
+#define CZ_GATE_TOKEN   2   /* y_dtype, one value an element */
+#define CZ_GATE_IDENTITY 0  /* act */
+#define CZ_GATE_SIGMOID  1
+#define CZ_GATE_SILU     2
+typedef struct {
+  int64_t rows, cols;         /* cols <= CZ_NORM_MAX_COLS                                  */
+  int32_t h_dtype;            /* of h, h_out, dh_in, dh                                    */
+  int32_t y_dtype;            /* of y, x, dx, dy, a token gate and its gradient            */
+  int32_t post_norm, pre_norm;/* whether each norm runs                                    */
+  int32_t gate_kind, gate_act;
+  float   h_scale, y_scale, eps;
+  int32_t accumulate;         /* backward: 1 adds to dw_post, dw_pre and a channel dgate   */
+  const float *w_post, *w_pre;/* cols values, nullable (ones)                              */
+  const void *gate;      int64_t ld_gate;    /* ld_gate: token gates only                  */
+  const void *h;         int64_t ld_h;       /* forward: the old stream; backward: h'      */
+  const void *y;         int64_t ld_y;
+  float *rstd_post, *rstd_pre;/* rows values: written by the forward (nullable), read by
+                                 the backward (needed for each norm that runs)             */
+  void *h_out;           int64_t ld_h_out;   /* forward: h' (nullable; may equal h)        */
+  void *x;               int64_t ld_x;       /* forward: nullable                          */
+  void *h_ckpt, *y_ckpt, *x_ckpt;            /* forward: checkpoints of h', y, x to write (nullable);
+                                                backward: h_ckpt and y_ckpt, where given, are
+                                                read in place of h and y                   */
+  const void *dx;        int64_t ld_dx;      /* backward: needed when pre_norm = 1         */
+  const void *dh_in;     int64_t ld_dh_in;   /* nullable (zero); may equal dh              */
+  void *dh;              int64_t ld_dh;      /* nullable                                   */
+  void *dy;              int64_t ld_dy;      /* nullable                                   */
+  void *dgate;           int64_t ld_dgate;   /* nullable; fp32 cols values, or y_dtype rows */
+  float *dw_post, *dw_pre;                   /* nullable, cols values                      */
+  void *workspace;       size_t workspace_bytes;   /* backward: cz_block_norm_workspace bytes,
+                                                      16-byte aligned, where dw_post, dw_pre or a
+                                                      channel dgate is asked for           */
+} cz_norm_args;
+/* All sizes and pointers zero, CZ_BF16, both norms on, no gate, scales 1, eps 1e-6. */
+void cz_norm_args_default(cz_norm_args* args);
+int cz_block_norm_workspace(int64_t rows, int64_t cols, size_t* bytes);
+int cz_block_norm_fwd(const cz_norm_args* args, void* stream);
+int cz_block_norm_bwd(const cz_norm_args* args, void* stream);
+
+/* Log probabilities of given tokens.  z = logits * inv_temp (inv_temp > 0), per row:
+ *   lse = log sum exp z;  logp = z[target] - lse;  entropy = lse - sum p z,  p = exp(z - lse)
+ *   the top_k largest z in descending order, ties to the lowest index: their ids and
+ *   log probabilities (a NaN ranks below everything).
+ * logits: dtype, rows x vocab, stride ld.  targets: device int64; a negative target is
+ * no token: logp 0 and no gradient through logp; one >= vocab gives logp NaN and a
+ * NaN gradient row.  Masked entries are -inf, or the lowest value of the type; a row of
+ * nothing but masked entries (its largest logit is below -1e37) has lse = -inf,
+ * logp = -inf, entropy 0, top_logp -inf and gradient 0.  A row with a NaN or +inf gives
+ * NaN.  z past the range of fp32 counts as infinite.  entropy, lse, top_ids/top_logp: nullable
+ * (top_k = 0: neither).  0 <= top_k <= min(vocab, CZ_LOGP_MAX_TOP).  logits == dlogits
+ * with equal strides computes the gradient in place.
+ * Backward, from lse (and, with g_entropy, entropy) of the forward:
+ *   dz[j] = inv_temp (g_logp (1[j = target] - p_j) - g_entropy p_j (log p_j + entropy)). */
+#define CZ_LOGP_MAX_TOP 32
+int cz_token_logp_fwd(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab, float inv_temp,
+                      const int64_t* targets, int32_t top_k, float* logp, float* entropy, float* lse,
+                      int64_t* top_ids, float* top_logp, void* stream);
+int cz_token_logp_bwd(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab, float inv_temp,
+                      const int64_t* targets, const float* lse, const float* entropy, const float* g_logp,
+                      const float* g_entropy, void* dlogits, int64_t ld_d, void* stream);
+
 /* Static string for a status code. */
 const char* cz_status_string(int status);
 
@@ -323,7 +439,7 @@ const char* cz_version(void);
 
 /* Support (no counterpart in the paper): name and description of the CUDA error
  * behind the most recent CZ_ERR_CUDA that a kernel launch of this thread's
- * cz_muon_step(_ex) calls returned ("cudaSuccess: no error" if none).  The
+ * cz_muon_step(_ex) or training-operator calls returned ("cudaSuccess: no error" if none).  The
  * string is owned by the library and valid until the thread's next call. */
 const char* cz_last_cuda_error(void);
 

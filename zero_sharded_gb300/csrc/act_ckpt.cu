@@ -1,0 +1,232 @@
+// Writing and reading 8-bit activation checkpoints (format: act_ckpt.cuh).
+//
+// Both directions are one pass over memory: s + 33/32 bytes an element (s = 2 for bf16,
+// 4 for fp32).  Rows on 16-byte boundaries take 8 elements a thread, a block of 32 being
+// 4 lanes; other strides take one element a lane, a block being a warp (one warp-wide
+// integer maximum), so that loads stay coalesced at any alignment.
+
+#include <cuda_runtime.h>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "act_ckpt.cuh"
+#include "train_ops.h"
+#include "vec8.cuh"
+
+namespace cz {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+
+// Chunk i of 8 elements: row and first column.
+__device__ __forceinline__ void chunk_at(int64_t i, uint32_t per_row, int64_t& row, int& col) {
+  if (i < (int64_t)0xFFFFFFFF) {
+    const uint32_t r = (uint32_t)i / per_row;
+    row = r;
+    col = (int)((uint32_t)i - r * per_row) * 8;
+  } else {
+    row = i / per_row;
+    col = (int)(i - row * per_row) * 8;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) encode8_kernel(const T* __restrict__ x, int64_t ld, int64_t n_chunks,
+                                                           int cols, uint8_t* __restrict__ ck, ActLayout l) {
+  const uint32_t per_row = (uint32_t)(l.ld_q / 8);
+  const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+  Raw8<T> raw[kUnroll];
+  int64_t row[kUnroll];
+  int col[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = i0 + u * kThreads;
+    zero8(raw[u]);
+    row[u] = -1;
+    if (i < n_chunks) {
+      chunk_at(i, per_row, row[u], col[u]);
+      if (col[u] < cols) load8(x + row[u] * ld + col[u], raw[u]);   // cols % 8 == 0 here
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    float v[8];
+    values8(raw[u], v);
+    uint2 q;
+    const uint32_t b = act_encode8(v, &q);
+    if (row[u] >= 0) {
+      *reinterpret_cast<uint2*>(ck + row[u] * l.ld_q + col[u]) = q;
+      if ((threadIdx.x & 3) == 0) ck[l.e_off + row[u] * l.ld_e + col[u] / kActBlock] = (uint8_t)b;
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) encode1_kernel(const T* __restrict__ x, int64_t ld, int64_t n_blocks,
+                                                           int cols, uint8_t* __restrict__ ck, ActLayout l) {
+  const uint32_t per_row = (uint32_t)(l.ld_q / kActBlock);
+  const int lane = threadIdx.x & 31;
+  const int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnroll;
+  float v[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = i0 + u, row = i / per_row;
+    const int c = (int)(i - row * per_row) * kActBlock + lane;
+    v[u] = (i < n_blocks && c < cols) ? load1(x + row * ld + c) : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = i0 + u, row = i / per_row;
+    uint32_t q;
+    const uint32_t b = act_encode1(v[u], &q);
+    if (i < n_blocks) {
+      const int blk = (int)(i - row * per_row);
+      ck[row * l.ld_q + blk * kActBlock + lane] = (uint8_t)q;
+      if (lane == 0) ck[l.e_off + row * l.ld_e + blk] = (uint8_t)b;
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) decode8_kernel(const uint8_t* __restrict__ ck, ActLayout l,
+                                                           int64_t n_chunks, int cols, T* __restrict__ x, int64_t ld) {
+  const uint32_t per_row = (uint32_t)(cols / 8);
+  const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+  uint2 q[kUnroll];
+  uint32_t b[kUnroll];
+  int64_t row[kUnroll];
+  int col[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = i0 + u * kThreads;
+    row[u] = -1;
+    if (i < n_chunks) {
+      chunk_at(i, per_row, row[u], col[u]);
+      q[u] = __ldcs(reinterpret_cast<const uint2*>(ck + row[u] * l.ld_q + col[u]));
+      b[u] = ck[l.e_off + row[u] * l.ld_e + col[u] / kActBlock];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    if (row[u] < 0) continue;
+    float v[8];
+    act_decode8(q[u], b[u], v);
+    store8(x + row[u] * ld + col[u], v);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) decode1_kernel(const uint8_t* __restrict__ ck, ActLayout l,
+                                                           int64_t n_blocks, int cols, T* __restrict__ x, int64_t ld) {
+  const uint32_t per_row = (uint32_t)(l.ld_q / kActBlock);
+  const int lane = threadIdx.x & 31;
+  const int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnroll;
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = i0 + u, row = i / per_row;
+    const int blk = (int)(i - row * per_row), c = blk * kActBlock + lane;
+    if (i < n_blocks && c < cols)
+      store1(x + row * ld + c, act_decode1(ck[row * l.ld_q + c], ck[l.e_off + row * l.ld_e + blk]));
+  }
+}
+
+bool sizes_ok(int64_t rows, int64_t cols) { return rows >= 0 && cols > 0 && rows < kMaxExtent && cols < kMaxExtent / 2; }
+
+// Blocks of a launch over n items, or 0 if they do not fit a grid.
+unsigned blocks_for(int64_t n, int64_t per_block) {
+  const int64_t b = div_up(n, per_block);
+  return b > INT32_MAX ? 0u : (unsigned)b;
+}
+
+template <typename T>
+int encode(const T* x, int64_t ld, int64_t rows, int64_t cols, uint8_t* ck, cudaStream_t s) {
+  const ActLayout l = act_layout(rows, cols);
+  if (cols % 8 == 0 && rows_aligned(x, ld, sizeof(T))) {
+    const int64_t n = rows * (l.ld_q / 8);
+    const unsigned g = blocks_for(n, kThreads * kUnroll);
+    return g ? launch_kernel(encode8_kernel<T>, g, kThreads, 0, s, 1, x, ld, n, (int)cols, ck, l) : CZ_ERR_UNSUPPORTED;
+  }
+  const int64_t n = rows * (l.ld_q / kActBlock);
+  const unsigned g = blocks_for(n, kThreads / 32 * kUnroll);
+  return g ? launch_kernel(encode1_kernel<T>, g, kThreads, 0, s, 1, x, ld, n, (int)cols, ck, l) : CZ_ERR_UNSUPPORTED;
+}
+
+template <typename T>
+int decode(const uint8_t* ck, int64_t rows, int64_t cols, T* x, int64_t ld, cudaStream_t s) {
+  const ActLayout l = act_layout(rows, cols);
+  if (cols % 8 == 0 && rows_aligned(x, ld, sizeof(T))) {
+    const int64_t n = rows * (cols / 8);
+    const unsigned g = blocks_for(n, kThreads * kUnroll);
+    return g ? launch_kernel(decode8_kernel<T>, g, kThreads, 0, s, 1, ck, l, n, (int)cols, x, ld) : CZ_ERR_UNSUPPORTED;
+  }
+  const int64_t n = rows * (l.ld_q / kActBlock);
+  const unsigned g = blocks_for(n, kThreads / 32 * kUnroll);
+  return g ? launch_kernel(decode1_kernel<T>, g, kThreads, 0, s, 1, ck, l, n, (int)cols, x, ld) : CZ_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+int check_sm103() {
+  static thread_local int known_dev = -1, known = CZ_OK;
+  int dev = 0;
+  if (note_cuda_error(cudaGetDevice(&dev)) != cudaSuccess) return CZ_ERR_CUDA;
+  if (dev == known_dev) return known;
+  int major = 0, minor = 0;
+  if (note_cuda_error(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess ||
+      note_cuda_error(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess)
+    return CZ_ERR_CUDA;
+  known = (major == 10 && minor == 3) ? CZ_OK : CZ_ERR_UNSUPPORTED;
+  known_dev = dev;
+  return known;
+}
+
+int sm_count() {
+  static thread_local int known_dev = -1, known = 1;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (dev == known_dev) return known;
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+  known = n;
+  known_dev = dev;
+  return known;
+}
+
+}  // namespace cz
+
+extern "C" int cz_act_size(int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes || !cz::sizes_ok(rows, cols)) return CZ_ERR_INVALID;
+  *bytes = (size_t)cz::act_layout(rows, cols).bytes;
+  return CZ_OK;
+}
+
+extern "C" int cz_act_encode(const void* x, int32_t dtype, int64_t ld, int64_t rows, int64_t cols, void* ckpt,
+                             void* stream) {
+  if (!cz::is_dtype(dtype) || !cz::sizes_ok(rows, cols) || !cz::matrix_ok(x, rows, cols, ld, cz::dtype_bytes(dtype)) ||
+      (!ckpt && rows > 0) || !cz::aligned(ckpt, 16))
+    return CZ_ERR_INVALID;
+  if (rows == 0) return CZ_OK;
+  const int st = cz::check_sm103();
+  if (st != CZ_OK) return st;
+  cz::NvtxRange range("cz/act_encode");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ck = static_cast<uint8_t*>(ckpt);
+  return dtype == CZ_F32 ? cz::encode(static_cast<const float*>(x), ld, rows, cols, ck, s)
+                         : cz::encode(static_cast<const __nv_bfloat16*>(x), ld, rows, cols, ck, s);
+}
+
+extern "C" int cz_act_decode(const void* ckpt, int64_t rows, int64_t cols, void* x, int32_t dtype, int64_t ld,
+                             void* stream) {
+  if (!cz::is_dtype(dtype) || !cz::sizes_ok(rows, cols) || !cz::matrix_ok(x, rows, cols, ld, cz::dtype_bytes(dtype)) ||
+      (!ckpt && rows > 0) || !cz::aligned(ckpt, 16))
+    return CZ_ERR_INVALID;
+  if (rows == 0) return CZ_OK;
+  const int st = cz::check_sm103();
+  if (st != CZ_OK) return st;
+  cz::NvtxRange range("cz/act_decode");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const uint8_t* ck = static_cast<const uint8_t*>(ckpt);
+  return dtype == CZ_F32 ? cz::decode(ck, rows, cols, static_cast<float*>(x), ld, s)
+                         : cz::decode(ck, rows, cols, static_cast<__nv_bfloat16*>(x), ld, s);
+}

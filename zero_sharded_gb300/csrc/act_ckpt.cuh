@@ -1,0 +1,111 @@
+// The 8-bit activation checkpoint: format and device code.
+//
+// A rows x cols matrix is kept as signed 8-bit integers q in blocks of 32 columns
+// that share a power of two: x^ = q * 2^E.  E is the smallest integer >= -126 with
+// max|x| <= 127 * 2^E, stored as the byte b = E + 127 (1 .. 249); q = x * 2^-E rounded to
+// nearest even, so |x^ - x| <= 2^(E-1) <= max|x| / 127.  A block that holds an
+// infinity or a NaN has b = 255 and decodes to NaN throughout.
+//
+// q has 7 bits and a sign, so x^ is exact in bf16 (8 significant bits) and in fp32: the
+// tensor cores read a checkpoint's values without a further rounding.  That is why
+// the scale is a power of two and not max|x| / 127 (which would lower the rms error by
+// a factor of 1.4 on Gaussian blocks).  32 columns: an outlier channel coarsens 31
+// neighbours only, and the bytes add 1/32 to the size.
+//
+// Buffer: rows of ld_q = round_up(cols, 32) q bytes (zeros past cols), then, from the next
+// multiple of 128 bytes, rows of ld_e = round_up(ld_q / 32, 16) scale bytes.  Both
+// strides are multiples of 16 bytes, as tensor copies need.
+#pragma once
+
+#include <stdint.h>
+
+namespace cz {
+
+constexpr int kActBlock = 32;
+
+struct ActLayout {
+  int64_t ld_q, ld_e, e_off, bytes;
+};
+
+inline ActLayout act_layout(int64_t rows, int64_t cols) {
+  ActLayout l;
+  l.ld_q = (cols + kActBlock - 1) / kActBlock * kActBlock;
+  l.ld_e = (l.ld_q / kActBlock + 15) / 16 * 16;
+  l.e_off = (rows * l.ld_q + 127) / 128 * 128;
+  l.bytes = l.e_off + rows * l.ld_e;
+  return l;
+}
+
+#ifdef __CUDACC__
+
+// Scale byte of a block from the bit pattern of max|x| (as unsigned: NaN > inf > finite).
+__device__ __forceinline__ uint32_t act_scale_byte(uint32_t amax_bits) {
+  const uint32_t ex = amax_bits >> 23;
+  if (ex == 255u) return 255u;
+  // amax = 1.f * 2^(ex-127) <= 127 * 2^E  <=>  E >= ex - 133, one more if 1.f > 127/64
+  const int b = (int)ex - 6 + ((amax_bits & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
+  return (uint32_t)max(b, 1);
+}
+
+// 2^-E of a scale byte; 0 for the byte of a non-finite block, whose q are all 0.
+__device__ __forceinline__ float act_inv_scale(uint32_t b) {
+  return b == 255u ? 0.f : __uint_as_float((254u - b) << 23);
+}
+
+// 2^E of a scale byte; NaN for the byte of a non-finite block.
+__device__ __forceinline__ float act_scale(uint32_t b) {
+  return b == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(b << 23);
+}
+
+// q of x as the low byte.  x * 2^-E is exact (or so small that it rounds to 0), and
+// adding 1.5 * 2^23 rounds it to the nearest even integer into the low mantissa bits.
+// At b = 249 (max|x| > 127 * 2^121) q is held to 63, so that q * 2^122 stays finite.
+__device__ __forceinline__ uint32_t act_quantise(float x, float inv, uint32_t b) {
+  float t = x * inv;
+  if (b >= 249u) t = b == 255u ? 0.f : fminf(fmaxf(t, -63.f), 63.f);
+  return __float_as_uint(t + 12582912.f) & 0xFFu;
+}
+
+// |x| as ordered bits.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// 8 consecutive elements of a row, the 4 lanes of an aligned group of 4 holding one
+// block: the group's scale byte, and the 8 q packed.  Every lane of the warp calls.
+__device__ __forceinline__ uint32_t act_encode8(const float* v, uint2* q) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t b = act_scale_byte(m);
+  const float inv = act_inv_scale(b);
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t q0 = act_quantise(v[4 * h], inv, b), q1 = act_quantise(v[4 * h + 1], inv, b);
+    const uint32_t q2 = act_quantise(v[4 * h + 2], inv, b), q3 = act_quantise(v[4 * h + 3], inv, b);
+    w[h] = q0 | (q1 << 8) | (q2 << 16) | (q3 << 24);
+  }
+  *q = make_uint2(w[0], w[1]);
+  return b;
+}
+
+// One element a lane, the warp's 32 lanes holding one block.  Every lane calls.
+__device__ __forceinline__ uint32_t act_encode1(float v, uint32_t* q) {
+  const uint32_t b = act_scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(v)));
+  *q = act_quantise(v, act_inv_scale(b), b);
+  return b;
+}
+
+__device__ __forceinline__ void act_decode8(uint2 q, uint32_t b, float* v) {
+  const float s = act_scale(b);
+  const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)(w[j >> 2] >> (8 * (j & 3))) * s;
+}
+
+__device__ __forceinline__ float act_decode1(uint8_t q, uint32_t b) { return (float)(int8_t)q * act_scale(b); }
+
+#endif  // __CUDACC__
+
+}  // namespace cz

@@ -1,0 +1,204 @@
+// Entry points of the block norms: checks, layout of rows over threads, launches.
+
+#include "block_norm.h"
+
+#include <algorithm>
+
+#include "train_ops.h"
+
+namespace cz {
+namespace {
+
+// Column sums of the backward are kept by at most this many blocks (four an SM).
+constexpr int kMaxBlocks = 608;
+
+bool flag(int32_t v) { return v == 0 || v == 1; }
+bool vector_ok(const void* p, uintptr_t bytes = 4) { return aligned(p, bytes); }
+
+// Whether [a, a + an) and [b, b + bn) share a byte.
+struct Span {
+  const void* p;
+  int64_t ld, bytes;   // bytes of an element
+};
+bool overlap(const Span& a, const Span& b, int64_t rows, int64_t cols) {
+  if (!a.p || !b.p || rows == 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t a1 = a0 + (uintptr_t)(((rows - 1) * a.ld + cols) * a.bytes),
+                  b1 = b0 + (uintptr_t)(((rows - 1) * b.ld + cols) * b.bytes);
+  return a0 < b1 && b0 < a1;
+}
+// An output may be an input only element for element.
+bool alias_ok(const Span& out, const Span& in, int64_t rows, int64_t cols) {
+  return (out.p == in.p && out.ld == in.ld) || !overlap(out, in, rows, cols);
+}
+
+int check_common(const cz_norm_args& a) {
+  if (a.rows < 0 || a.rows >= kMaxExtent || a.cols < 1 || a.cols > CZ_NORM_MAX_COLS) return CZ_ERR_INVALID;
+  if (!is_dtype(a.h_dtype) || !is_dtype(a.y_dtype) || !flag(a.post_norm) || !flag(a.pre_norm) || !flag(a.accumulate))
+    return CZ_ERR_INVALID;
+  if (a.gate_kind < CZ_GATE_NONE || a.gate_kind > CZ_GATE_TOKEN || a.gate_act < CZ_GATE_IDENTITY || a.gate_act > CZ_GATE_SILU)
+    return CZ_ERR_INVALID;
+  if (!std::isfinite(a.h_scale) || !std::isfinite(a.y_scale) || !(a.eps >= 0.f) || !std::isfinite(a.eps)) return CZ_ERR_INVALID;
+  if (!vector_ok(a.w_post) || !vector_ok(a.w_pre) || !vector_ok(a.rstd_post) || !vector_ok(a.rstd_pre) ||
+      !vector_ok(a.dw_post) || !vector_ok(a.dw_pre) || !vector_ok(a.h_ckpt, 16) || !vector_ok(a.y_ckpt, 16) ||
+      !vector_ok(a.x_ckpt, 16))
+    return CZ_ERR_INVALID;
+  const int64_t yb = dtype_bytes(a.y_dtype);
+  if (a.gate_kind == CZ_GATE_CHANNEL && (!a.gate || !vector_ok(a.gate))) return CZ_ERR_INVALID;
+  if (a.gate_kind == CZ_GATE_TOKEN && !matrix_ok(a.gate, a.rows, a.cols, a.ld_gate, yb)) return CZ_ERR_INVALID;
+  return CZ_OK;
+}
+
+bool opt_matrix_ok(const void* p, const cz_norm_args& a, int64_t ld, int64_t bytes) {
+  return p == nullptr || matrix_ok(p, a.rows, a.cols, ld, bytes);
+}
+
+NormParams params_of(const cz_norm_args& a) {
+  NormParams p{};
+  p.rows = a.rows;
+  p.cols = (int32_t)a.cols;
+  // 8 elements a thread while a row fits 512 threads, then 16: a row of the backward holds
+  // six fp32 values an element in registers
+  const int64_t per = a.cols <= 8 * 512 ? 8 : 16;
+  p.row_threads = (int32_t)round_up(div_up(a.cols, per), 32);
+  p.rows_per_block = std::max(1, 256 / p.row_threads);   // narrow rows share a block of up to 8 warps
+  p.post = a.post_norm;
+  p.pre = a.pre_norm;
+  p.gate_kind = a.gate_kind;
+  p.gate_act = a.gate_act;
+  p.h_scale = a.h_scale;
+  p.y_scale = a.y_scale;
+  p.eps = a.eps;
+  p.h = a.h;
+  p.y = a.y;
+  p.gate = a.gate_kind == CZ_GATE_NONE ? nullptr : a.gate;
+  p.ld_h = a.ld_h;
+  p.ld_y = a.ld_y;
+  p.ld_gate = a.gate_kind == CZ_GATE_TOKEN ? a.ld_gate : 0;
+  p.w_post = a.w_post;
+  p.w_pre = a.w_pre;
+  p.rstd_post = a.rstd_post;
+  p.rstd_pre = a.rstd_pre;
+  p.h_ckpt = static_cast<uint8_t*>(a.h_ckpt);
+  p.y_ckpt = static_cast<uint8_t*>(a.y_ckpt);
+  p.x_ckpt = static_cast<uint8_t*>(a.x_ckpt);
+  p.ck = act_layout(a.rows, a.cols);
+  return p;
+}
+
+}  // namespace
+}  // namespace cz
+
+using namespace cz;
+
+extern "C" void cz_norm_args_default(cz_norm_args* args) {
+  if (!args) return;
+  *args = cz_norm_args{};
+  args->post_norm = args->pre_norm = 1;
+  args->h_scale = args->y_scale = 1.f;
+  args->eps = 1e-6f;
+}
+
+extern "C" int cz_block_norm_workspace(int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes || rows < 0 || rows >= kMaxExtent || cols < 1 || cols > CZ_NORM_MAX_COLS) return CZ_ERR_INVALID;
+  *bytes = (size_t)(std::max<int64_t>(1, std::min<int64_t>(rows, kMaxBlocks)) * 3 * cols * 4);
+  return CZ_OK;
+}
+
+extern "C" int cz_block_norm_fwd(const cz_norm_args* args, void* stream) {
+  if (!args) return CZ_ERR_INVALID;
+  const cz_norm_args& a = *args;
+  const int st = check_common(a);
+  if (st != CZ_OK) return st;
+  const int64_t hb = dtype_bytes(a.h_dtype), yb = dtype_bytes(a.y_dtype);
+  if (!matrix_ok(a.h, a.rows, a.cols, a.ld_h, hb) || !matrix_ok(a.y, a.rows, a.cols, a.ld_y, yb) ||
+      !opt_matrix_ok(a.h_out, a, a.ld_h_out, hb) || !opt_matrix_ok(a.x, a, a.ld_x, yb))
+    return CZ_ERR_INVALID;
+  if (!a.pre_norm && (a.x || a.x_ckpt)) return CZ_ERR_INVALID;
+  const Span h{a.h, a.ld_h, hb}, y{a.y, a.ld_y, yb}, ho{a.h_out, a.ld_h_out, hb}, x{a.x, a.ld_x, yb};
+  if (!alias_ok(ho, h, a.rows, a.cols) || overlap(ho, y, a.rows, a.cols) || overlap(x, h, a.rows, a.cols) ||
+      overlap(x, y, a.rows, a.cols) || overlap(x, ho, a.rows, a.cols))
+    return CZ_ERR_INVALID;
+  if (a.rows == 0) return CZ_OK;
+  const int dev = check_sm103();
+  if (dev != CZ_OK) return dev;
+  NvtxRange range("cz/block_norm_fwd");
+  NormParams p = params_of(a);
+  p.h_out = a.h_out;
+  p.x = a.x;
+  p.ld_h_out = a.ld_h_out;
+  p.ld_x = a.ld_x;
+  const bool vec = a.cols % 8 == 0 && rows_aligned(a.h, a.ld_h, hb) && rows_aligned(a.y, a.ld_y, yb) &&
+                   rows_aligned(a.h_out, a.ld_h_out, hb) && rows_aligned(a.x, a.ld_x, yb) &&
+                   (a.gate_kind != CZ_GATE_TOKEN || rows_aligned(a.gate, a.ld_gate, yb));
+  return launch_norm_fwd(p, a.h_dtype == CZ_F32, a.y_dtype == CZ_F32, vec, stream);
+}
+
+extern "C" int cz_block_norm_bwd(const cz_norm_args* args, void* stream) {
+  if (!args) return CZ_ERR_INVALID;
+  const cz_norm_args& a = *args;
+  const int st = check_common(a);
+  if (st != CZ_OK) return st;
+  const int64_t hb = dtype_bytes(a.h_dtype), yb = dtype_bytes(a.y_dtype);
+  const bool channel = a.gate_kind == CZ_GATE_CHANNEL, token = a.gate_kind == CZ_GATE_TOKEN;
+  // y is read by the post-norm and by the gate's gradient, h' by the pre-norm
+  const bool need_y = a.post_norm || (a.gate_kind != CZ_GATE_NONE && a.dgate);
+  if (a.rows > 0) {
+    if (need_y && !a.y && !a.y_ckpt) return CZ_ERR_INVALID;
+    if (a.pre_norm && ((!a.h && !a.h_ckpt) || !a.dx || !a.rstd_pre)) return CZ_ERR_INVALID;
+    if (a.post_norm && !a.rstd_post) return CZ_ERR_INVALID;
+  }
+  if (!a.pre_norm && (a.dx || a.dw_pre)) return CZ_ERR_INVALID;
+  if (!a.post_norm && a.dw_post) return CZ_ERR_INVALID;
+  if (a.gate_kind == CZ_GATE_NONE && a.dgate) return CZ_ERR_INVALID;
+  if (!opt_matrix_ok(a.h, a, a.ld_h, hb) || !opt_matrix_ok(a.y, a, a.ld_y, yb) || !opt_matrix_ok(a.dx, a, a.ld_dx, yb) ||
+      !opt_matrix_ok(a.dh_in, a, a.ld_dh_in, hb) || !opt_matrix_ok(a.dh, a, a.ld_dh, hb) ||
+      !opt_matrix_ok(a.dy, a, a.ld_dy, yb))
+    return CZ_ERR_INVALID;
+  if (token && !opt_matrix_ok(a.dgate, a, a.ld_dgate, yb)) return CZ_ERR_INVALID;
+  if (channel && !vector_ok(a.dgate)) return CZ_ERR_INVALID;
+  const Span h{a.h_ckpt ? nullptr : a.h, a.ld_h, hb}, y{a.y_ckpt ? nullptr : a.y, a.ld_y, yb}, dx{a.dx, a.ld_dx, yb},
+      di{a.dh_in, a.ld_dh_in, hb}, g{token ? a.gate : nullptr, a.ld_gate, yb}, dh{a.dh, a.ld_dh, hb},
+      dy{a.dy, a.ld_dy, yb}, dg{token ? a.dgate : nullptr, a.ld_dgate, yb};
+  for (const Span* in : {&h, &y, &dx, &g})
+    for (const Span* out : {&dh, &dy, &dg})
+      if (overlap(*out, *in, a.rows, a.cols)) return CZ_ERR_INVALID;
+  if (!alias_ok(dh, di, a.rows, a.cols) || overlap(dy, di, a.rows, a.cols) || overlap(dg, di, a.rows, a.cols) ||
+      overlap(dh, dy, a.rows, a.cols) || overlap(dh, dg, a.rows, a.cols) || overlap(dy, dg, a.rows, a.cols))
+    return CZ_ERR_INVALID;
+  float* dgate = channel ? static_cast<float*>(a.dgate) : nullptr;
+  const bool sums = a.dw_post || a.dw_pre || dgate;
+  if (sums) {
+    size_t need = 0;
+    cz_block_norm_workspace(a.rows, a.cols, &need);
+    if (!a.workspace || a.workspace_bytes < need) return CZ_ERR_NOMEM;
+    if (!aligned(a.workspace, 16)) return CZ_ERR_INVALID;
+  }
+  const int dev = check_sm103();
+  if (dev != CZ_OK) return dev;
+  NvtxRange range("cz/block_norm_bwd");
+  NormParams p = params_of(a);
+  p.dx = a.dx;
+  p.dh_in = a.dh_in;
+  p.dh = a.dh;
+  p.dy = a.dy;
+  p.dgate = token ? a.dgate : nullptr;
+  p.ld_dx = a.ld_dx;
+  p.ld_dh_in = a.ld_dh_in;
+  p.ld_dh = a.ld_dh;
+  p.ld_dy = a.ld_dy;
+  p.ld_dgate = a.ld_dgate;
+  p.partial = sums ? static_cast<float*>(a.workspace) : nullptr;
+  const bool vec = a.cols % 8 == 0 && (p.h_ckpt || rows_aligned(a.h, a.ld_h, hb)) &&
+                   (p.y_ckpt || rows_aligned(a.y, a.ld_y, yb)) && rows_aligned(a.dx, a.ld_dx, yb) &&
+                   rows_aligned(a.dh_in, a.ld_dh_in, hb) && rows_aligned(a.dh, a.ld_dh, hb) &&
+                   rows_aligned(a.dy, a.ld_dy, yb) &&
+                   (!token || (rows_aligned(a.gate, a.ld_gate, yb) && rows_aligned(a.dgate, a.ld_dgate, yb)));
+  const int blocks = (int)std::min<int64_t>(div_up(a.rows, p.rows_per_block), std::min(kMaxBlocks, 2 * sm_count()));
+  if (blocks > 0) {
+    const int r = launch_norm_bwd(p, a.h_dtype == CZ_F32, a.y_dtype == CZ_F32, vec, blocks, stream);
+    if (r != CZ_OK) return r;
+  }
+  if (!sums) return CZ_OK;
+  return launch_norm_fold(p.partial, blocks, p.cols, a.dw_post, a.dw_pre, dgate, a.accumulate, stream);
+}

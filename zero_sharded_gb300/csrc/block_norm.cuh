@@ -1,0 +1,177 @@
+// Device code shared by the forward and backward block norms.
+//
+// A row's elements are spread over `row_threads` threads, 8*C each.  VEC: element
+// (c, j) of thread t is column (c*row_threads + t)*8 + j, so that 8 elements move with
+// 16-byte accesses and 4 lanes hold one checkpoint block; otherwise column
+// (c*8 + j)*row_threads + t, one element a lane, a warp holding one block.
+#pragma once
+
+#include "act_ckpt.cuh"
+#include "block_norm.h"
+#include "vec8.cuh"
+
+namespace cz {
+
+template <bool VEC>
+__device__ __forceinline__ int col_of(int c, int j, int t, int n) {
+  return VEC ? (c * n + t) * 8 + j : (c * 8 + j) * n + t;
+}
+
+// Sum of v over the threads of a row.  One warp a row needs no shared memory; otherwise
+// `red` holds a float for every warp of the block and the block synchronises once, so
+// consecutive sums alternate between two such arrays.
+__device__ __forceinline__ float row_sum(float v, float* red, int row_warps) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if (row_warps == 1) return v;
+  const int warp = threadIdx.x >> 5, first = warp / row_warps * row_warps;
+  if ((threadIdx.x & 31) == 0) red[warp] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int i = 0; i < row_warps; ++i) s += red[first + i];
+  return s;
+}
+
+__device__ __forceinline__ float gate_value(float g, int act) {
+  if (act == CZ_GATE_IDENTITY) return g;
+  const float s = 1.f / (1.f + __expf(-g));
+  return act == CZ_GATE_SIGMOID ? s : g * s;
+}
+
+// act(g) and act'(g).
+__device__ __forceinline__ void gate_value_slope(float g, int act, float& value, float& slope) {
+  if (act == CZ_GATE_IDENTITY) {
+    value = g;
+    slope = 1.f;
+    return;
+  }
+  const float s = 1.f / (1.f + __expf(-g));
+  const float one_less = 1.f / (1.f + __expf(g));   // 1 - s without cancellation
+  if (act == CZ_GATE_SIGMOID) {
+    value = s;
+    slope = s * one_less;
+  } else {
+    value = g * s;
+    slope = s * (1.f + g * one_less);
+  }
+}
+
+// 8 elements of a chunk from a matrix row (VEC) or from strided columns.
+template <typename T, bool VEC>
+struct Chunk;
+template <typename T>
+struct Chunk<T, true> {
+  Raw8<T> r;
+  __device__ __forceinline__ void load(const T* row, int c, int t, int n, int cols) {
+    const int col = col_of<true>(c, 0, t, n);
+    if (col < cols) load8(row + col, r); else zero8(r);
+  }
+  __device__ __forceinline__ void values(float* v) const { values8(r, v); }
+};
+template <typename T>
+struct Chunk<T, false> {
+  float v8[8];
+  __device__ __forceinline__ void load(const T* row, int c, int t, int n, int cols) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = col_of<false>(c, j, t, n);
+      v8[j] = col < cols ? load1(row + col) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void values(float* v) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v8[j];
+  }
+};
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_chunk(T* row, const float* v, int c, int t, int n, int cols) {
+  if constexpr (VEC) {
+    const int col = col_of<true>(c, 0, t, n);
+    if (col < cols) store8(row + col, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = col_of<false>(c, j, t, n);
+      if (col < cols) store1(row + col, v[j]);
+    }
+  }
+}
+
+// 8 elements of a vector over the columns (fp32, any alignment): stays in the first-level
+// cache, every row of the block reads it again.
+template <bool VEC>
+__device__ __forceinline__ void load_vector(const float* w, bool vec16, float* v, int c, int t, int n, int cols) {
+  if constexpr (VEC) {
+    const int col = col_of<true>(c, 0, t, n);
+    if (col < cols) {
+      if (vec16) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(w + col)), b = __ldg(reinterpret_cast<const float4*>(w + col) + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __ldg(w + col + j);
+      }
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = col_of<false>(c, j, t, n);
+      v[j] = col < cols ? __ldg(w + col) : 0.f;
+    }
+  }
+}
+
+// Writes the chunk's part of a checkpoint row; every lane of the warp calls, `live` says
+// whether the row exists.
+template <bool VEC>
+__device__ __forceinline__ void keep_chunk(uint8_t* ck, const ActLayout& l, int64_t row, bool live, const float* v, int c,
+                                           int t, int n) {
+  if constexpr (VEC) {
+    uint2 q;
+    const uint32_t b = act_encode8(v, &q);
+    const int col = col_of<true>(c, 0, t, n);
+    if (live && col < l.ld_q) {
+      *reinterpret_cast<uint2*>(ck + row * l.ld_q + col) = q;
+      if ((t & 3) == 0) ck[l.e_off + row * l.ld_e + col / kActBlock] = (uint8_t)b;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t q;
+      const uint32_t b = act_encode1(v[j], &q);
+      const int col = col_of<false>(c, j, t, n);
+      if (live && col < l.ld_q) {
+        ck[row * l.ld_q + col] = (uint8_t)q;
+        if ((t & 31) == 0) ck[l.e_off + row * l.ld_e + col / kActBlock] = (uint8_t)b;
+      }
+    }
+  }
+}
+
+// The chunk's values of a kept row.
+template <bool VEC>
+__device__ __forceinline__ void kept_chunk(const uint8_t* ck, const ActLayout& l, int64_t row, float* v, int c, int t, int n) {
+  if constexpr (VEC) {
+    const int col = col_of<true>(c, 0, t, n);
+    if (col < l.ld_q) {
+      act_decode8(__ldcs(reinterpret_cast<const uint2*>(ck + row * l.ld_q + col)),
+                  ck[l.e_off + row * l.ld_e + col / kActBlock], v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = col_of<false>(c, j, t, n);
+      v[j] = col < l.ld_q ? act_decode1(ck[row * l.ld_q + col], ck[l.e_off + row * l.ld_e + col / kActBlock]) : 0.f;
+    }
+  }
+}
+
+}  // namespace cz

@@ -6,6 +6,7 @@
 
 #include <vector>
 
+#include <cuda_runtime_api.h>
 #include <nvtx3/nvToolsExt.h>
 
 #include "cz.h"
@@ -59,5 +60,8 @@ int muon_step(const cz_plan* plan, int32_t rank, float* flat_param, const void* 
 // or null if no such call has set it up there; cz_device_status(stream, NULL)
 // reads and clears its status word.
 void* noalloc_scratch_if_set_up();
+
+// Keeps a CUDA error for cz_last_cuda_error of this thread; returns it.
+cudaError_t note_cuda_error(cudaError_t e);
 
 }  // namespace cz

@@ -994,6 +994,9 @@ int get_internal_ws(size_t need, void** out, bool capturing) {
 }
 
 }  // namespace
+
+cudaError_t note_cuda_error(cudaError_t e) { return note(e); }
+
 }  // namespace cz
 
 using namespace cz;

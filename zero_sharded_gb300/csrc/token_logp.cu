@@ -1,0 +1,481 @@
+// Log probabilities of given tokens with entropy and top alternatives, and the gradient.
+//
+// Forward, z = x inv_temp, m = max x, c = inv_temp log2(e), d_j = (x_j - m) c:
+//   s = sum 2^d_j,  w = sum 2^d_j d_j,  lse = m inv_temp + ln s,  entropy = ln s - ln2 w / s
+// in one pass over the row: every thread keeps (m, s, w) of the elements it has seen and
+// rescales s and w when its maximum grows; the threads', warps' and cluster blocks'
+// triples are joined in a fixed order.  x - m is formed before the scale, so that rows of a
+// type's lowest value and masked -inf entries stay finite; d is held to >= -150, where
+// 2^d is 0, so that a masked entry's 2^d d is 0 and not NaN.
+//
+// Top alternatives cost no second pass: the k-th largest of the maxima of groups of 8
+// threads (disjoint parts of the row) is a bound that the k largest elements reach, so only threads whose
+// own maximum reaches it read their part again and put forward what does.  Keys of (value,
+// complement of the index) make the order total.  Should ties or a skewed row
+// put forward more than the buffer holds, k rounds of a block-wide maximum below the last
+// key find them instead.
+//
+// Backward is elementwise: p = exp(z - lse).  Bound by memory both ways: s bytes an
+// element forward, 2 s backward.
+
+#include <cuda_runtime.h>
+
+#include "train_ops.h"
+#include "vec8.cuh"
+
+namespace cz {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kGroups = kWarps * 4;       // groups of 8 threads
+constexpr int kCand = 1024;               // candidates that the buffer holds
+constexpr float kMasked = -1e37f;         // a largest logit below this: -inf or a type's lowest value throughout
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+static_assert(kGroups >= CZ_LOGP_MAX_TOP, "the bound needs top_k groups");
+
+template <typename T>
+struct Vec;                                // 16 bytes of elements
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  __device__ static void values(uint4 r, float* v) { unpack8(r, v); }
+  __device__ static uint4 pack(const float* v) { return pack8(v); }
+};
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  __device__ static void values(uint4 r, float* v) {
+    v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y);
+    v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
+  }
+  __device__ static uint4 pack(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Softmax sums of a set of elements: maximum, sum of 2^d and of 2^d d.
+struct Sums {
+  float m, s, w;
+};
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c) {
+  Sums r;
+  r.m = max_nan(a.m, b.m);
+  if (r.m == -INFINITY) return Sums{-INFINITY, 0.f, 0.f};
+  const float da = fmaxf((a.m - r.m) * c, -150.f), db = fmaxf((b.m - r.m) * c, -150.f);
+  const float fa = exp2_fast(da), fb = exp2_fast(db);
+  r.s = a.s * fa + b.s * fb;
+  r.w = fa * (a.w + a.s * da) + fb * (b.w + b.s * db);
+  return r;
+}
+
+// One element more.
+__device__ __forceinline__ void add_one(Sums& a, float x, float c) { a = join(a, Sums{x, x == -INFINITY ? 0.f : 1.f, 0.f}, c); }
+
+// Order of the alternatives: larger value first, then the lower index; NaN last.
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
+  uint32_t o = 0;
+  if (x == x) {
+    o = __float_as_uint(x + 0.f);                       // -0 counts as 0
+    o = (o & 0x80000000u) ? ~o : (o | 0x80000000u);
+  }
+  return ((uint64_t)o << 32) | (uint32_t)~index;
+}
+__device__ __forceinline__ float value_of(uint64_t key) {
+  const uint32_t o = (uint32_t)(key >> 32);
+  if (o == 0) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+
+// A row as 16-byte vectors between a head and a tail of single elements.
+template <typename T>
+struct Row {
+  const T* p;
+  int64_t vocab;
+  int head, nv, tail0;       // elements before the first vector, vectors, first element after them
+  __device__ Row(const T* base, int64_t n) : p(base), vocab(n) {
+    const int off = (int)((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(T));
+    head = (int)min((int64_t)((Vec<T>::N - off) % Vec<T>::N), n);
+    nv = (int)((n - head) / Vec<T>::N);
+    tail0 = head + nv * Vec<T>::N;
+  }
+  __device__ int singles() const { return head + (int)(vocab - tail0); }
+  __device__ int single_at(int i) const { return i < head ? i : tail0 + i - head; }
+};
+
+// Calls f(value, index) on every element of thread t's share of vectors [v0, v1), and on its
+// single element if `singles`.
+template <typename T, typename F>
+__device__ __forceinline__ void each(const Row<T>& r, int v0, int v1, bool singles, F f) {
+  for (int i = v0 + (int)threadIdx.x; i < v1; i += kThreads) {
+    float v[Vec<T>::N];
+    Vec<T>::values(__ldg(reinterpret_cast<const uint4*>(r.p + r.head) + i), v);
+#pragma unroll
+    for (int j = 0; j < Vec<T>::N; ++j) f(v[j], (uint32_t)(r.head + i * Vec<T>::N + j));
+  }
+  if (singles && (int)threadIdx.x < r.singles()) {
+    const int at = r.single_at(threadIdx.x);
+    f(load1(r.p + at), (uint32_t)at);
+  }
+}
+
+struct LogpShared {
+  uint64_t cand[kCand];
+  uint64_t top[CZ_LOGP_MAX_TOP];
+  uint64_t best[kWarps];
+  float group[kGroups];
+  Sums warp[kWarps];
+  Sums all;
+  int n_cand;
+};
+
+__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+
+// The k largest keys of this block's part into sh.top, in order (0 past its elements).
+// own_max: the thread's largest element, NaN if it saw one.
+template <typename T>
+__device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool singles, float own_max, int k) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float g = own_max;
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, d));
+  if ((lane & 7) == 0) sh.group[warp * 4 + (lane >> 3)] = g;
+  if (threadIdx.x == 0) sh.n_cand = 0;
+  if ((int)threadIdx.x < k) sh.top[threadIdx.x] = 0;
+  __syncthreads();
+  // the k-th largest group maximum (every warp for itself)
+  const float ga = sh.group[lane], gb = sh.group[lane + 32];
+  int ra = 0, rb = 0;
+#pragma unroll 8
+  for (int i = 0; i < kGroups; ++i) {
+    const float o = sh.group[i];
+    ra += (o > ga || (o == ga && i < lane)) ? 1 : 0;
+    rb += (o > gb || (o == gb && i < lane + 32)) ? 1 : 0;
+  }
+  const bool nan = __any_sync(0xffffffffu, ga != ga || gb != gb);
+  const uint32_t ha = __ballot_sync(0xffffffffu, ra == k - 1), hb = __ballot_sync(0xffffffffu, rb == k - 1);
+  const float bound = ha ? __shfl_sync(0xffffffffu, ga, __ffs(ha) - 1) : __shfl_sync(0xffffffffu, gb, max(__ffs(hb) - 1, 0));
+  if (!nan) {
+    if (own_max >= bound)
+      each(r, v0, v1, singles, [&](float x, uint32_t i) {
+        if (x >= bound) {
+          const int at = atomicAdd(&sh.n_cand, 1);
+          if (at < kCand) sh.cand[at] = key_of(x, i);
+        }
+      });
+    __syncthreads();
+    const int n = sh.n_cand;
+    if (n <= kCand) {
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t mine = sh.cand[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += sh.cand[j] > mine ? 1 : 0;
+        if (rank < k) sh.top[rank] = mine;
+      }
+      __syncthreads();
+      return;
+    }
+  }
+  // more candidates than the buffer holds, or NaN: one block-wide maximum after another
+  uint64_t last = ~0ull;
+  for (int q = 0; q < k; ++q) {
+    uint64_t mine = 0;
+    each(r, v0, v1, singles, [&](float x, uint32_t i) {
+      const uint64_t key = key_of(x, i);
+      if (key < last) mine = max_u64(mine, key);
+    });
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mine = max_u64(mine, __shfl_xor_sync(0xffffffffu, mine, d));
+    __syncthreads();                       // the last round's readers of sh.best are done
+    if (lane == 0) sh.best[warp] = mine;
+    __syncthreads();
+    mine = 0;
+    for (int i = 0; i < kWarps; ++i) mine = max_u64(mine, sh.best[i]);
+    last = mine;
+    if (threadIdx.x == 0) sh.top[q] = mine;
+    if (mine == 0) break;                  // fewer elements than k in this part
+  }
+  __syncthreads();
+}
+
+struct FwdParams {
+  const void* logits;
+  int64_t ld, vocab;
+  float inv_temp;
+  const int64_t* targets;
+  int32_t top_k;
+  float *logp, *entropy, *lse;
+  int64_t* top_ids;
+  float* top_logp;
+};
+
+// A row is taken by a cluster of blocks (one block when there are enough rows).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) logp_fwd_kernel(const __grid_constant__ FwdParams p, int parts) {
+  __shared__ LogpShared sh;
+  const int64_t row = blockIdx.x / parts;
+  const int part = (int)(blockIdx.x - row * parts);
+  const Row<T> r(static_cast<const T*>(p.logits) + row * p.ld, p.vocab);
+  const int per = (r.nv + parts - 1) / parts;
+  const int v0 = min(r.nv, part * per), v1 = min(r.nv, v0 + per);
+  const float c = p.inv_temp * kLog2e;
+  constexpr int N = Vec<T>::N;
+  constexpr int U = 4;
+
+  Sums a{-INFINITY, 0.f, 0.f};
+  const uint4* body = reinterpret_cast<const uint4*>(r.p + r.head);
+  for (int i = v0 + (int)threadIdx.x; i < v1; i += U * kThreads) {
+    uint4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * kThreads < v1) raw[u] = __ldg(body + i + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u * kThreads >= v1) break;
+      float v[N];
+      Vec<T>::values(raw[u], v);
+      float m = v[0];
+#pragma unroll
+      for (int j = 1; j < N; ++j) m = max_nan(m, v[j]);
+      if (!(m <= a.m)) {                       // grown (or NaN): bring the sums to the new maximum
+        const float nm = max_nan(m, a.m);
+        const float d = fmaxf((a.m - nm) * c, -150.f), f = exp2_fast(d);
+        a.w = f * (a.w + a.s * d);
+        a.s *= f;
+        a.m = nm;
+      }
+      const float base = a.m == -INFINITY ? 0.f : a.m;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float d = max_nan((v[j] - base) * c, -150.f), e = exp2_fast(d);
+        a.s += e;
+        a.w = fmaf(e, d, a.w);
+      }
+    }
+  }
+  if (part == 0 && (int)threadIdx.x < r.singles()) add_one(a, load1(r.p + r.single_at(threadIdx.x)), c);
+  const float own_max = a.m;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    Sums o;
+    o.m = __shfl_xor_sync(0xffffffffu, a.m, d);
+    o.s = __shfl_xor_sync(0xffffffffu, a.s, d);
+    o.w = __shfl_xor_sync(0xffffffffu, a.w, d);
+    a = (lane & d) ? join(o, a, c) : join(a, o, c);      // the same order in both lanes
+  }
+  if (lane == 0) sh.warp[warp] = a;
+  if (p.top_k > 0) block_top<T>(sh, r, v0, v1, part == 0, own_max, p.top_k);
+  else __syncthreads();
+  if (threadIdx.x == 0) {
+    a = sh.warp[0];
+    for (int i = 1; i < kWarps; ++i) a = join(a, sh.warp[i], c);
+    sh.all = a;
+  }
+  if (parts > 1) cluster_sync();
+  else __syncthreads();
+
+  if (part == 0) {
+    a = sh.all;
+    if (parts > 1) {
+      const uint32_t all = smem_u32(&sh.all);
+      for (int q = 1; q < parts; ++q) {
+        const uint32_t at = mapa_shared(all, (uint32_t)q);
+        Sums o;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.m) : "r"(at) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.s) : "r"(at + 4) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.w) : "r"(at + 8) : "memory");
+        a = join(a, o, c);
+      }
+    }
+    const float zm = a.m * p.inv_temp;
+    const bool empty = a.m <= kMasked || zm == -INFINITY;   // nothing but masked entries
+    const float ln_s = zm == INFINITY ? __uint_as_float(0x7FC00000u) : logf(a.s);
+    const float lse = empty ? -INFINITY : zm + ln_s;
+    // from the maximum and not from lse, which may be too large to resolve ln s
+    auto log_p = [&](float x) { return empty ? -INFINITY : fmaf(x - a.m, p.inv_temp, -ln_s); };
+    if (threadIdx.x == 0) {
+      const int64_t t = p.targets[row];
+      float lp = 0.f;
+      if (t >= p.vocab) lp = __uint_as_float(0x7FC00000u);
+      else if (t >= 0) lp = log_p(load1(r.p + t));
+      p.logp[row] = lp;
+      if (p.lse) p.lse[row] = lse;
+      if (p.entropy) p.entropy[row] = empty ? 0.f : ln_s - kLn2 * (a.w / a.s);
+    }
+    const int k = p.top_k;
+    if (parts == 1) {
+      if ((int)threadIdx.x < k) {
+        const uint64_t key = sh.top[threadIdx.x];
+        p.top_ids[row * k + threadIdx.x] = (uint32_t)~(uint32_t)key;
+        p.top_logp[row * k + threadIdx.x] = log_p(value_of(key));
+      }
+    } else if (k > 0) {
+      // the parts' lists side by side; a key's place is the number of larger ones
+      const int n = parts * k;
+      if ((int)threadIdx.x < n) {
+        const int q = threadIdx.x / k;
+        const uint32_t at = mapa_shared(smem_u32(&sh.top[threadIdx.x - q * k]), (uint32_t)q);
+        uint64_t key;
+        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(key) : "r"(at) : "memory");
+        sh.cand[threadIdx.x] = key;
+      }
+      __syncthreads();
+      if ((int)threadIdx.x < n) {
+        const uint64_t mine = sh.cand[threadIdx.x];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += sh.cand[j] > mine ? 1 : 0;
+        if (mine != 0 && rank < k) {
+          p.top_ids[row * k + rank] = (uint32_t)~(uint32_t)mine;
+          p.top_logp[row * k + rank] = log_p(value_of(mine));
+        }
+      }
+    }
+  }
+  if (parts > 1) cluster_sync();             // the first block has read the others' shared memory
+}
+
+struct BwdParams {
+  const void* logits;
+  void* d;
+  int64_t ld, ld_d, vocab;
+  float inv_temp;
+  const int64_t* targets;
+  const float *lse, *entropy, *g_logp, *g_entropy;
+};
+
+constexpr int kBwdThreads = 256;
+constexpr int kBwdUnroll = 4;
+
+// VEC: the row of logits and the row of gradients lie alike within 16 bytes.
+template <typename T>
+__global__ void __launch_bounds__(kBwdThreads) logp_bwd_kernel(const __grid_constant__ BwdParams p, int parts) {
+  const int64_t row = blockIdx.x / parts;
+  const int part = (int)(blockIdx.x - row * parts);
+  constexpr int N = Vec<T>::N;
+  const Row<T> r(static_cast<const T*>(p.logits) + row * p.ld, p.vocab);
+  T* out = static_cast<T*>(p.d) + row * p.ld_d;
+  const float lse = p.lse[row];
+  const int64_t target = p.targets[row];
+  float g = (p.g_logp && target >= 0) ? p.g_logp[row] : 0.f;
+  if (target >= p.vocab) g = __uint_as_float(0x7FC00000u);
+  const float ge = p.g_entropy ? p.g_entropy[row] : 0.f;
+  const bool empty = lse == -INFINITY;
+  const float k1 = -p.inv_temp * ge;
+  const float k0 = -p.inv_temp * (ge != 0.f ? fmaf(ge, p.entropy[row], g) : g);
+  const float hot = p.inv_temp * g;
+  auto grad = [&](float x, int64_t j) {
+    const float lp = max_nan(fmaf(x, p.inv_temp, -lse), -200.f);
+    float d = exp2_fast(lp * kLog2e) * fmaf(k1, lp, k0);
+    if (j == target) d += hot;
+    return empty ? 0.f : d;
+  };
+  const bool alike = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(r.p)) & 15) == 0;
+  if (alike) {
+    const uint4* body = reinterpret_cast<const uint4*>(r.p + r.head);
+    uint4* to = reinterpret_cast<uint4*>(out + r.head);
+    const int i0 = part * (kBwdThreads * kBwdUnroll) + (int)threadIdx.x;
+    uint4 raw[kBwdUnroll];
+#pragma unroll
+    for (int u = 0; u < kBwdUnroll; ++u)
+      if (i0 + u * kBwdThreads < r.nv) raw[u] = ld_stream16(body + i0 + u * kBwdThreads);
+#pragma unroll
+    for (int u = 0; u < kBwdUnroll; ++u) {
+      const int i = i0 + u * kBwdThreads;
+      if (i >= r.nv) break;
+      float v[N];
+      Vec<T>::values(raw[u], v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = grad(v[j], (int64_t)r.head + (int64_t)i * N + j);
+      to[i] = Vec<T>::pack(v);
+    }
+    if (part == 0 && (int)threadIdx.x < r.singles()) {
+      const int at = r.single_at(threadIdx.x);
+      store1(out + at, grad(load1(r.p + at), at));
+    }
+  } else {
+    const int64_t j0 = (int64_t)part * (kBwdThreads * kBwdUnroll * N);
+    const int64_t j1 = min(p.vocab, j0 + kBwdThreads * kBwdUnroll * N);
+    for (int64_t j = j0 + threadIdx.x; j < j1; j += kBwdThreads) store1(out + j, grad(load1(r.p + j), j));
+  }
+}
+
+bool rows_vocab_ok(int64_t rows, int64_t vocab) { return rows >= 0 && rows < kMaxExtent && vocab >= 1 && vocab < kMaxExtent / 2; }
+
+template <typename T>
+int fwd(const FwdParams& p, int64_t rows, cudaStream_t s) {
+  // few rows: up to 8 blocks a row, while each keeps two vectors a thread
+  int parts = 1;
+  const int64_t vectors = p.vocab / Vec<T>::N;
+  while (parts < 8 && rows * parts < 2 * (int64_t)sm_count() && vectors >= (int64_t)parts * 4 * kThreads) parts *= 2;
+  if (rows * parts > INT32_MAX) return CZ_ERR_UNSUPPORTED;
+  return launch_kernel(logp_fwd_kernel<T>, dim3((unsigned)(rows * parts)), kThreads, 0, s, parts, p, parts);
+}
+
+template <typename T>
+int bwd(const BwdParams& p, int64_t rows, cudaStream_t s) {
+  // one vector more than vocab holds when a row starts inside one
+  const int64_t parts = div_up(div_up(p.vocab, Vec<T>::N), (int64_t)kBwdThreads * kBwdUnroll);
+  if (rows * parts > INT32_MAX) return CZ_ERR_UNSUPPORTED;
+  return launch_kernel(logp_bwd_kernel<T>, dim3((unsigned)(rows * parts)), kBwdThreads, 0, s, 1, p, (int)parts);
+}
+
+}  // namespace
+}  // namespace cz
+
+using namespace cz;
+
+extern "C" int cz_token_logp_fwd(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
+                                 float inv_temp, const int64_t* targets, int32_t top_k, float* logp, float* entropy,
+                                 float* lse, int64_t* top_ids, float* top_logp, void* stream) {
+  if (!is_dtype(dtype) || !rows_vocab_ok(rows, vocab) || !matrix_ok(logits, rows, vocab, ld, dtype_bytes(dtype)))
+    return CZ_ERR_INVALID;
+  if (!std::isfinite(inv_temp) || inv_temp <= 0.f || top_k < 0 || top_k > CZ_LOGP_MAX_TOP || top_k > vocab) return CZ_ERR_INVALID;
+  if (!aligned(targets, 8) || !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(lse, 4) || !aligned(top_ids, 8) ||
+      !aligned(top_logp, 4))
+    return CZ_ERR_INVALID;
+  if (rows == 0) return CZ_OK;
+  if (!targets || !logp || (top_k > 0 && (!top_ids || !top_logp))) return CZ_ERR_INVALID;
+  const int st = check_sm103();
+  if (st != CZ_OK) return st;
+  NvtxRange range("cz/token_logp_fwd");
+  const FwdParams p{logits, ld, vocab, inv_temp, targets, top_k, logp, entropy, lse, top_ids, top_logp};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return dtype == CZ_F32 ? fwd<float>(p, rows, s) : fwd<__nv_bfloat16>(p, rows, s);
+}
+
+extern "C" int cz_token_logp_bwd(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
+                                 float inv_temp, const int64_t* targets, const float* lse, const float* entropy,
+                                 const float* g_logp, const float* g_entropy, void* dlogits, int64_t ld_d,
+                                 void* stream) {
+  if (!is_dtype(dtype) || !rows_vocab_ok(rows, vocab) || !matrix_ok(logits, rows, vocab, ld, dtype_bytes(dtype)) ||
+      !matrix_ok(dlogits, rows, vocab, ld_d, dtype_bytes(dtype)))
+    return CZ_ERR_INVALID;
+  if (!std::isfinite(inv_temp) || inv_temp <= 0.f || (g_entropy && !entropy)) return CZ_ERR_INVALID;
+  if (!aligned(targets, 8) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4))
+    return CZ_ERR_INVALID;
+  if (rows == 0) return CZ_OK;
+  if (!targets || !lse) return CZ_ERR_INVALID;
+  // in place is element for element; any other overlap would read what was written
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(logits), b0 = reinterpret_cast<uintptr_t>(dlogits);
+  const uintptr_t an = (uintptr_t)(((rows - 1) * ld + vocab) * dtype_bytes(dtype)),
+                  bn = (uintptr_t)(((rows - 1) * ld_d + vocab) * dtype_bytes(dtype));
+  if (!(a0 == b0 && ld == ld_d) && a0 < b0 + bn && b0 < a0 + an) return CZ_ERR_INVALID;
+  const int st = check_sm103();
+  if (st != CZ_OK) return st;
+  NvtxRange range("cz/token_logp_bwd");
+  const BwdParams p{logits, dlogits, ld, ld_d, vocab, inv_temp, targets, lse, entropy, g_logp, g_entropy};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return dtype == CZ_F32 ? bwd<float>(p, rows, s) : bwd<__nv_bfloat16>(p, rows, s);
+}

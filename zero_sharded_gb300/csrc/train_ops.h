@@ -1,0 +1,67 @@
+// Host-side helpers shared by the training-step operators (activation
+// checkpoints, block norms, token log probabilities).  Not part of the C-ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include <utility>
+
+#include "cz_internal.h"
+
+namespace cz {
+
+inline bool is_dtype(int32_t t) { return t == CZ_BF16 || t == CZ_F32; }
+inline int64_t dtype_bytes(int32_t t) { return t == CZ_F32 ? 4 : 2; }
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Largest row, column and stride counts the operators take: products of two stay
+// far inside 64 bits.
+constexpr int64_t kMaxExtent = int64_t{1} << 31;
+
+// A rows x cols matrix of `bytes`-byte elements at p, rows ld elements apart: whether
+// the pointer is there and aligned to its elements, and the stride holds a row.
+inline bool matrix_ok(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t bytes) {
+  if (!aligned(p, (uintptr_t)bytes) || ld < cols || ld >= kMaxExtent) return false;
+  return p != nullptr || rows == 0;
+}
+
+// Whether 8 elements at a time can be read or written with 16-byte accesses: every
+// row starts on a 16-byte boundary.
+inline bool rows_aligned(const void* p, int64_t ld, int64_t bytes) {
+  return p == nullptr || (aligned(p, 16) && (ld * bytes) % 16 == 0);
+}
+
+// CZ_OK on an sm_103 device; the answer is looked up once per device.
+int check_sm103();
+// Streaming multiprocessors of the current device (looked up once per device).
+int sm_count();
+
+// Launches `kernel`; the status comes from this launch alone, not from an error that an
+// earlier call left behind.
+template <typename... KArgs, typename... Args>
+int launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster,
+                  Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (cluster > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  return note_cuda_error(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...)) == cudaSuccess ? CZ_OK
+                                                                                                       : CZ_ERR_CUDA;
+}
+
+}  // namespace cz

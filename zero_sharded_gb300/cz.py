@@ -26,6 +26,7 @@ CZ_ERR_UNSUPPORTED = -7
 _i64p = ctypes.POINTER(ctypes.c_int64)
 _i32p = ctypes.POINTER(ctypes.c_int32)
 _f64p = ctypes.POINTER(ctypes.c_double)
+_vp = ctypes.c_void_p
 
 
 class cz_step_opts(ctypes.Structure):
@@ -41,6 +42,32 @@ class cz_step_opts(ctypes.Structure):
         ("workspace_bytes", ctypes.c_size_t),
         ("debug_update_out", ctypes.c_void_p),
         ("lr_device", ctypes.c_void_p),
+    ]
+
+
+class cz_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+        ("h_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+        ("post_norm", ctypes.c_int32), ("pre_norm", ctypes.c_int32),
+        ("gate_kind", ctypes.c_int32), ("gate_act", ctypes.c_int32),
+        ("h_scale", ctypes.c_float), ("y_scale", ctypes.c_float), ("eps", ctypes.c_float),
+        ("accumulate", ctypes.c_int32),
+        ("w_post", _vp), ("w_pre", _vp),
+        ("gate", _vp), ("ld_gate", ctypes.c_int64),
+        ("h", _vp), ("ld_h", ctypes.c_int64),
+        ("y", _vp), ("ld_y", ctypes.c_int64),
+        ("rstd_post", _vp), ("rstd_pre", _vp),
+        ("h_out", _vp), ("ld_h_out", ctypes.c_int64),
+        ("x", _vp), ("ld_x", ctypes.c_int64),
+        ("h_ckpt", _vp), ("y_ckpt", _vp), ("x_ckpt", _vp),
+        ("dx", _vp), ("ld_dx", ctypes.c_int64),
+        ("dh_in", _vp), ("ld_dh_in", ctypes.c_int64),
+        ("dh", _vp), ("ld_dh", ctypes.c_int64),
+        ("dy", _vp), ("ld_dy", ctypes.c_int64),
+        ("dgate", _vp), ("ld_dgate", ctypes.c_int64),
+        ("dw_post", _vp), ("dw_pre", _vp),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -106,6 +133,23 @@ def load() -> ctypes.CDLL:
                                             ctypes.c_void_p, ctypes.c_void_p]),
         "cz_apply_update": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, _i64p, _i64p,
                                            ctypes.c_int64, ctypes.c_float, ctypes.c_int32, ctypes.c_void_p]),
+        "cz_act_size": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]),
+        "cz_act_encode": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _vp,
+                                         _vp]),
+        "cz_act_decode": (ctypes.c_int, [_vp, ctypes.c_int64, ctypes.c_int64, _vp, ctypes.c_int32, ctypes.c_int64,
+                                         _vp]),
+        "cz_act_wgrad_workspace": (ctypes.c_int, [_vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                  ctypes.POINTER(ctypes.c_size_t)]),
+        "cz_act_wgrad": (ctypes.c_int, [_vp, ctypes.c_int64, _vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _vp,
+                                        _vp, ctypes.c_int32, _vp, ctypes.c_size_t, _vp]),
+        "cz_norm_args_default": (None, [ctypes.POINTER(cz_norm_args)]),
+        "cz_block_norm_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]),
+        "cz_block_norm_fwd": (ctypes.c_int, [ctypes.POINTER(cz_norm_args), _vp]),
+        "cz_block_norm_bwd": (ctypes.c_int, [ctypes.POINTER(cz_norm_args), _vp]),
+        "cz_token_logp_fwd": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                             ctypes.c_float, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp, _vp]),
+        "cz_token_logp_bwd": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                             ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int64, _vp]),
         "cz_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "cz_version": (ctypes.c_char_p, []),
         "cz_last_cuda_error": (ctypes.c_char_p, []),
@@ -389,3 +433,240 @@ def cz_apply_update(flat_param, param_bf16, flat_update, offsets: Sequence[int],
     _check("cz_apply_update", load().cz_apply_update(_ptr(flat_param), _ptr(param_bf16), _ptr(flat_update),
                                                      _i64(offsets), _shapes_flat(shapes), len(offsets), float(lr),
                                                      1 if shape_scale else 0, _stream_ptr(stream)))
+
+
+# ---------------------------------------------------------------- operators of a training step
+# Matrices are 2-D tensors whose rows are dense (stride 1) and any distance apart; sizes and types are
+# taken from the tensors and checked against one another, the rest of the checks are the library's.
+CZ_BF16, CZ_F32 = 0, 1
+CZ_NORM_MAX_COLS = 16384
+CZ_LOGP_MAX_TOP = 32
+GATE_ACTS = {"identity": 0, "sigmoid": 1, "silu": 2}
+_DTYPES: dict = {}
+
+
+class _Torch:
+    """torch, imported when the first of these operators is called (the planner's callers need none)."""
+
+    def __getattr__(self, name):
+        import torch
+
+        self.bfloat16, self.float32, self.int64 = torch.bfloat16, torch.float32, torch.int64
+        _DTYPES.update({torch.bfloat16: CZ_BF16, torch.float32: CZ_F32})
+        return getattr(torch, name)
+
+
+torch = _Torch()
+
+
+def _dtype(fn: str, t) -> int:
+    d = _DTYPES.get(t.dtype) if torch.float32 else None
+    if d is None:
+        raise CzError(fn, CZ_ERR_INVALID, f"type {t.dtype}: bfloat16 or float32 is wanted")
+    return d
+
+
+def _mat(fn: str, name: str, t, rows: int, cols: int, dtype=None) -> Tuple[Optional[int], int]:
+    """(pointer, row stride) of a rows x cols tensor; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.shape != (rows, cols) or (dtype is not None and t.dtype != dtype):
+        raise CzError(fn, CZ_ERR_INVALID, f"{name}: {tuple(t.shape)} {t.dtype}, wanted {(rows, cols)} {dtype or ''}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise CzError(fn, CZ_ERR_INVALID, f"{name}: the elements of a row are not next to one another")
+    return t.data_ptr(), (ld if rows > 1 else cols)
+
+
+def _vec(fn: str, name: str, t, n: int, dtype=None) -> Optional[int]:
+    """Pointer of a dense tensor of n elements (fp32 unless another type is named); None for None."""
+    if t is None:
+        return None
+    dtype = dtype or torch.float32
+    if t.numel() != n or t.dtype != dtype or not t.is_contiguous():
+        raise CzError(fn, CZ_ERR_INVALID, f"{name}: {tuple(t.shape)} {t.dtype}, wanted {n} dense {dtype}")
+    return t.data_ptr()
+
+
+def _bytes(fn: str, name: str, t, n: int) -> Optional[int]:
+    """Pointer of a dense buffer of at least n bytes; None for None."""
+    if t is None:
+        return None
+    if t.numel() * t.element_size() < n or not t.is_contiguous():
+        raise CzError(fn, CZ_ERR_NOMEM, f"{name}: {t.numel() * t.element_size()} bytes, {n} are needed")
+    return t.data_ptr()
+
+
+def cz_act_size(rows: int, cols: int) -> int:
+    """Bytes of the 8-bit checkpoint of a rows x cols activation."""
+    n = ctypes.c_size_t(0)
+    _check("cz_act_size", load().cz_act_size(int(rows), int(cols), ctypes.byref(n)))
+    return n.value
+
+
+def _ckpt(fn: str, name: str, t, rows: int, cols: int) -> Optional[int]:
+    return None if t is None else _bytes(fn, name, t, cz_act_size(rows, cols))
+
+
+def cz_act_encode(x, ckpt, stream=None) -> None:
+    """Keeps x (bf16 or fp32, 2-D) in 8 bits: ckpt is a device buffer of cz_act_size(*x.shape) bytes."""
+    fn = "cz_act_encode"
+    rows, cols = x.shape
+    p, ld = _mat(fn, "x", x, rows, cols)
+    _check(fn, load().cz_act_encode(p, _dtype(fn, x), ld, rows, cols, _ckpt(fn, "ckpt", ckpt, rows, cols),
+                                    _stream_ptr(stream)))
+
+
+def cz_act_decode(ckpt, x, stream=None) -> None:
+    """Reads a checkpoint's values into x."""
+    fn = "cz_act_decode"
+    rows, cols = x.shape
+    p, ld = _mat(fn, "x", x, rows, cols)
+    _check(fn, load().cz_act_decode(_ckpt(fn, "ckpt", ckpt, rows, cols), rows, cols, p, _dtype(fn, x), ld,
+                                    _stream_ptr(stream)))
+
+
+def cz_act_wgrad_workspace(dy, n_in: int) -> int:
+    """Bytes of workspace for the weight gradient of these dy (rows x n_out)."""
+    fn = "cz_act_wgrad_workspace"
+    rows, n_out = dy.shape
+    p, ld = _mat(fn, "dy", dy, rows, n_out, torch.bfloat16)
+    n = ctypes.c_size_t(0)
+    _check(fn, load().cz_act_wgrad_workspace(p, ld, rows, n_out, int(n_in), ctypes.byref(n)))
+    return n.value
+
+
+def cz_act_wgrad(dy, ckpt, out, add=None, workspace=None, stream=None) -> None:
+    """out[n_out, n_in] = add + dy^T x^ from the checkpoint of x (rows x n_in).  out: a dense fp32 or bf16 tensor,
+    such as a view of the flat gradient buffer; add may be out (accumulates in place)."""
+    fn = "cz_act_wgrad"
+    rows, n_out = dy.shape
+    p, ld = _mat(fn, "dy", dy, rows, n_out, torch.bfloat16)
+    if out.dim() != 2 or out.shape[0] != n_out:
+        raise CzError(fn, CZ_ERR_INVALID, f"out: {tuple(out.shape)}, wanted {n_out} rows")
+    n_in = out.shape[1]
+    o = _vec(fn, "out", out, n_out * n_in, out.dtype)
+    a = _vec(fn, "add", add, n_out * n_in, out.dtype)
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(fn, load().cz_act_wgrad(p, ld, _ckpt(fn, "ckpt", ckpt, rows, n_in), rows, n_out, n_in, a, o, _dtype(fn, out),
+                                   _ptr(workspace), ws, _stream_ptr(stream)))
+
+
+def cz_norm_args_default() -> cz_norm_args:
+    a = cz_norm_args()
+    load().cz_norm_args_default(ctypes.byref(a))
+    return a
+
+
+def cz_block_norm_workspace(rows: int, cols: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("cz_block_norm_workspace", load().cz_block_norm_workspace(int(rows), int(cols), ctypes.byref(n)))
+    return n.value
+
+
+def _norm_common(fn, rows, cols, h_dtype, y_dtype, w_post, w_pre, gate, gate_act, h_scale, y_scale, eps, post_norm,
+                 pre_norm, rstd_post, rstd_pre):
+    for d in (h_dtype, y_dtype):
+        if torch.float32 and d not in _DTYPES:
+            raise CzError(fn, CZ_ERR_INVALID, f"type {d}: bfloat16 or float32 is wanted")
+    if gate_act not in GATE_ACTS:
+        raise CzError(fn, CZ_ERR_INVALID, f"gate_act {gate_act!r}: one of {', '.join(GATE_ACTS)} is wanted")
+    a = cz_norm_args()
+    a.rows, a.cols = rows, cols
+    a.h_dtype, a.y_dtype = _DTYPES[h_dtype], _DTYPES[y_dtype]
+    a.post_norm, a.pre_norm = int(bool(post_norm)), int(bool(pre_norm))
+    a.h_scale, a.y_scale, a.eps = h_scale, y_scale, eps
+    a.w_post, a.w_pre = _vec(fn, "w_post", w_post, cols), _vec(fn, "w_pre", w_pre, cols)
+    a.rstd_post, a.rstd_pre = _vec(fn, "rstd_post", rstd_post, rows), _vec(fn, "rstd_pre", rstd_pre, rows)
+    if gate is not None:
+        a.gate_act = GATE_ACTS[gate_act]
+        if gate.dim() == 1:
+            a.gate_kind, a.gate = 1, _vec(fn, "gate", gate, cols)
+        else:
+            a.gate_kind = 2
+            a.gate, a.ld_gate = _mat(fn, "gate", gate, rows, cols, y_dtype)
+    return a
+
+
+def cz_block_norm_fwd(h, y, h_out=None, x=None, w_post=None, w_pre=None, gate=None, gate_act: str = "identity",
+                      h_scale: float = 1.0, y_scale: float = 1.0, eps: float = 1e-6, post_norm: bool = True,
+                      pre_norm: bool = True, rstd_post=None, rstd_pre=None, h_ckpt=None, y_ckpt=None, x_ckpt=None,
+                      stream=None) -> None:
+    """h' = h_scale h + y_scale act(gate) norm(y) w_post; x = norm(h') w_pre.  A 1-D gate (fp32) has one value a
+    column, a 2-D gate (the type of y) one an element.  rstd_*, *_ckpt: written where given."""
+    fn = "cz_block_norm_fwd"
+    rows, cols = h.shape
+    a = _norm_common(fn, rows, cols, h.dtype, y.dtype, w_post, w_pre, gate, gate_act, h_scale, y_scale, eps, post_norm,
+                     pre_norm, rstd_post, rstd_pre)
+    a.h, a.ld_h = _mat(fn, "h", h, rows, cols)
+    a.y, a.ld_y = _mat(fn, "y", y, rows, cols)
+    a.h_out, a.ld_h_out = _mat(fn, "h_out", h_out, rows, cols, h.dtype)
+    a.x, a.ld_x = _mat(fn, "x", x, rows, cols, y.dtype)
+    a.h_ckpt, a.y_ckpt, a.x_ckpt = (_ckpt(fn, n, t, rows, cols) for n, t in
+                                    (("h_ckpt", h_ckpt), ("y_ckpt", y_ckpt), ("x_ckpt", x_ckpt)))
+    _check(fn, load().cz_block_norm_fwd(ctypes.byref(a), _stream_ptr(stream)))
+
+
+def cz_block_norm_bwd(h, y, dx, dh_in, dh, dy, w_post=None, w_pre=None, gate=None, gate_act: str = "identity",
+                      h_scale: float = 1.0, y_scale: float = 1.0, post_norm: bool = True, pre_norm: bool = True,
+                      rstd_post=None, rstd_pre=None, h_ckpt=None, y_ckpt=None, dw_post=None, dw_pre=None, dgate=None,
+                      accumulate: bool = False, workspace=None, stream=None) -> None:
+    """Gradients of h (dh), y (dy), the weights and the gate from those of x (dx) and h' (dh_in).  h is the forward's
+    h'; h_ckpt and y_ckpt, where given, are read in place of h and y (which may then be None).  Each gradient is
+    computed where a tensor is given for it; dw_post, dw_pre and a channel gate's dgate need a workspace."""
+    fn = "cz_block_norm_bwd"
+    some = next((t for t in (dh, dy, dx, dh_in, h, y) if t is not None), None)
+    if some is None:
+        raise CzError(fn, CZ_ERR_INVALID, "no tensor gives the sizes")
+    rows, cols = some.shape
+    h_type = next((t.dtype for t in (dh, dh_in, h) if t is not None), some.dtype)
+    y_type = next((t.dtype for t in (dy, dx, y) if t is not None), some.dtype)
+    a = _norm_common(fn, rows, cols, h_type, y_type, w_post, w_pre, gate, gate_act, h_scale, y_scale, 0.0, post_norm,
+                     pre_norm, rstd_post, rstd_pre)
+    a.accumulate = int(bool(accumulate))
+    a.h, a.ld_h = _mat(fn, "h", h, rows, cols, h_type)
+    a.y, a.ld_y = _mat(fn, "y", y, rows, cols, y_type)
+    a.h_ckpt, a.y_ckpt = _ckpt(fn, "h_ckpt", h_ckpt, rows, cols), _ckpt(fn, "y_ckpt", y_ckpt, rows, cols)
+    a.dx, a.ld_dx = _mat(fn, "dx", dx, rows, cols, y_type)
+    a.dh_in, a.ld_dh_in = _mat(fn, "dh_in", dh_in, rows, cols, h_type)
+    a.dh, a.ld_dh = _mat(fn, "dh", dh, rows, cols, h_type)
+    a.dy, a.ld_dy = _mat(fn, "dy", dy, rows, cols, y_type)
+    if dgate is not None:
+        if gate is None or gate.dim() == 1:
+            a.dgate = _vec(fn, "dgate", dgate, cols)
+        else:
+            a.dgate, a.ld_dgate = _mat(fn, "dgate", dgate, rows, cols, y_type)
+    a.dw_post, a.dw_pre = _vec(fn, "dw_post", dw_post, cols), _vec(fn, "dw_pre", dw_pre, cols)
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(fn, load().cz_block_norm_bwd(ctypes.byref(a), _stream_ptr(stream)))
+
+
+def cz_token_logp_fwd(logits, targets, logp, entropy=None, lse=None, top_ids=None, top_logp=None,
+                      inv_temp: float = 1.0, stream=None) -> None:
+    """Log probability of each row's target under softmax(logits * inv_temp), with the entropy, the log of the sum
+    and, by the width of top_ids (int64) and top_logp, the most likely tokens."""
+    fn = "cz_token_logp_fwd"
+    rows, vocab = logits.shape
+    p, ld = _mat(fn, "logits", logits, rows, vocab)
+    k = 0 if top_ids is None else top_ids.shape[1]
+    if (top_ids is None) != (top_logp is None):
+        raise CzError(fn, CZ_ERR_INVALID, "top_ids and top_logp go together")
+    _check(fn, load().cz_token_logp_fwd(
+        p, _dtype(fn, logits), ld, rows, vocab, inv_temp, _vec(fn, "targets", targets, rows, torch.int64), k,
+        _vec(fn, "logp", logp, rows), _vec(fn, "entropy", entropy, rows), _vec(fn, "lse", lse, rows),
+        _vec(fn, "top_ids", top_ids, rows * k, torch.int64) if k else None,
+        _vec(fn, "top_logp", top_logp, rows * k) if k else None, _stream_ptr(stream)))
+
+
+def cz_token_logp_bwd(logits, targets, lse, dlogits, entropy=None, g_logp=None, g_entropy=None, inv_temp: float = 1.0,
+                      stream=None) -> None:
+    """Gradient of the logits from those of logp and entropy; dlogits may be logits."""
+    fn = "cz_token_logp_bwd"
+    rows, vocab = logits.shape
+    p, ld = _mat(fn, "logits", logits, rows, vocab)
+    d, ld_d = _mat(fn, "dlogits", dlogits, rows, vocab, logits.dtype)
+    _check(fn, load().cz_token_logp_bwd(
+        p, _dtype(fn, logits), ld, rows, vocab, inv_temp, _vec(fn, "targets", targets, rows, torch.int64),
+        _vec(fn, "lse", lse, rows), _vec(fn, "entropy", entropy, rows), _vec(fn, "g_logp", g_logp, rows),
+        _vec(fn, "g_entropy", g_entropy, rows), d, ld_d, _stream_ptr(stream)))
