@@ -1,8 +1,26 @@
 // Weight gradient from an 8-bit activation checkpoint (format: act_ckpt.cuh):
-//   out[n][k] = add[n][k] + sum_t dy[t][n] x^[t][k]
-// One 64 x 64 tile of out a block, sums in fp32.
+//   out[n][k] = add[n][k] + sum_t dy[t][n] x^[t][k],  x^ = q 2^E
+// on the 5th-generation tensor cores.  x^ is exact in bf16, so the product is bf16 x bf16 with
+// fp32 sums, and reading 33/32 bytes an element in place of 2 only adds the decoding.
+//
+// Both operands lie with their outer dimension contiguous (the sum runs over rows), so both are
+// MN-major in shared memory.  A CTA pair (cta_group::2) computes a 256 x 256 tile of out in steps of
+// 64 tokens; each CTA holds 128 columns of dy and 128 of x^ a step and receives 128 rows of the tile.  Per CTA:
+//   warp 0       TMA producer: dy (128-byte swizzle), q and its scale bytes, a ring of stages
+//   warp 1       TMEM allocation (two 256-column accumulators) and, in the even CTA, the thread that
+//                issues tcgen05.mma
+//   warps 2-5    epilogue: tcgen05.ld, 32 x 32 blocks through shared memory so that rows of out are
+//                read (add) and written 128 bytes at a time
+//   warps 6-13   decoders: 16 q at a time from shared memory to swizzled bf16 in the stage
+// A byte q becomes bf16 without integer conversion: 0x4300 | (q & 127) is 128 + (q & 127), 0x4300 | (q & 128)
+// is 128 or 256, and their difference is q (exact); one more multiplication applies 2^E (exact).
+// Per pair of elements: a byte permutation, two masks, a difference and a product.
 
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
 
 #include "act_ckpt.cuh"
 #include "train_ops.h"
@@ -11,45 +29,403 @@
 namespace cz {
 namespace {
 
-constexpr int kTile = 64, kDepth = 16, kThreads = 256;
+constexpr int kTile = 256;                 // rows and columns of a pair's tile
+constexpr int kDepth = 64;                 // tokens a step
+constexpr int kStages = 5;
+constexpr int kBytesA = 128 * kDepth * 2, kBytesB = 128 * kDepth * 2, kBytesQ = 128 * kDepth, kBytesE = 16 * kDepth;
+constexpr int kStageBytes = kBytesA + kBytesB + kBytesQ + kBytesE;
+constexpr int kEpiWarps = 4, kDecWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps + kDecWarps);
+constexpr int kEpiPitch = 36;              // floats of a staged row: 16-byte accesses without bank conflicts
+constexpr int kEpiBytes = 32 * kEpiPitch * 4;
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kEpiBytes + 512;
+constexpr uint32_t kTmemCols = 512;
+constexpr int64_t kTimeoutNs = 2000000000LL;
+static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
-template <typename TO>
-__global__ void __launch_bounds__(kThreads) wgrad_kernel(const __nv_bfloat16* __restrict__ dy, int64_t ld_dy,
-                                                         const uint8_t* __restrict__ ck, ActLayout l, int64_t rows,
-                                                         int64_t n_out, int64_t n_in, const TO* add, TO* out) {
-  __shared__ float sa[kDepth][kTile], sb[kDepth][kTile];
-  const int64_t n0 = (int64_t)blockIdx.y * kTile, k0 = (int64_t)blockIdx.x * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t t0 = 0; t0 < rows; t0 += kDepth) {
-    for (int i = threadIdx.x; i < kDepth * kTile; i += kThreads) {
-      const int64_t t = t0 + i / kTile;
-      const int c = i % kTile;
-      sa[i / kTile][c] = (t < rows && n0 + c < n_out) ? load1(dy + t * ld_dy + n0 + c) : 0.f;
-      sb[i / kTile][c] = (t < rows && k0 + c < n_in)
-                             ? act_decode1(ck[t * l.ld_q + k0 + c], ck[l.e_off + t * l.ld_e + (k0 + c) / kActBlock])
-                             : 0.f;
-    }
-    __syncthreads();
+struct WgradParams {
+  CUtensorMap dy, q, e;
+  const void* add;
+  void* out;
+  int32_t* status;
+  int64_t n_out, n_in;
+  int32_t nk;                // steps of a whole tile
+  int32_t tiles_m, tiles_n;  // tiles over n_out and n_in
+  int32_t units;             // CTA pairs
+  int32_t out_f32, vec;      // vec: rows of out and add can be accessed 16 bytes at a time
+};
+
+// Tile t of the raster: groups of 8 tile rows, so that the tiles in flight share few panels of either operand.
+__device__ __forceinline__ void tile_at(const WgradParams& p, int t, int& tm, int& tn) {
+  const int group = 8 * p.tiles_n, g = t / group, first = g * 8;
+  const int height = min(8, p.tiles_m - first), r = t - g * group;
+  tm = first + r % height;
+  tn = r / height;
+}
+
+struct Smem {
+  uint8_t* stage;
+  float* epi;
+  uint64_t *full_a, *full_q, *decoded, *empty, *tfull, *tempty, *drain;
+  uint32_t* tmem;
+  int* abort;
+};
+
+__device__ __forceinline__ Smem carve(uint8_t* raw) {
+  Smem s;
+  uint8_t* p = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  s.stage = p;
+  p += kStages * kStageBytes;
+  s.epi = reinterpret_cast<float*>(p);
+  p += kEpiWarps * kEpiBytes;
+  uint64_t* b = reinterpret_cast<uint64_t*>(p);
+  s.full_a = b;
+  s.full_q = b + kStages;
+  s.decoded = b + 2 * kStages;
+  s.empty = b + 3 * kStages;
+  s.tfull = b + 4 * kStages;
+  s.tempty = s.tfull + 2;
+  s.drain = s.tempty + 2;
+  s.tmem = reinterpret_cast<uint32_t*>(s.drain + 1);
+  s.abort = reinterpret_cast<int*>(s.drain + 2);
+  return s;
+}
+
+// 4 q bytes to 4 bf16 values q * s.
+__device__ __forceinline__ uint2 decode4(uint32_t w, uint32_t scale2) {
+  uint32_t r[2];
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[d][ty * 4 + i], sb[d][tx + 16 * j], acc[i][j]);
-    __syncthreads();
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t p = __byte_perm(w, 0x43434343u, h ? 0x4342 : 0x4140);
+    const uint32_t a = p & 0xFF7FFF7Fu, b = p & 0xFF80FF80u;
+    asm("{\n\t.reg .b32 d;\n\tsub.rn.bf16x2 d, %1, %2;\n\tmul.rn.bf16x2 %0, d, %3;\n\t}" : "=r"(r[h]) : "r"(a), "r"(b), "r"(scale2));
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = n0 + ty * 4 + i, k = k0 + tx + 16 * j;
-      if (n < n_out && k < n_in) store1(out + n * n_in + k, acc[i][j] + (add ? load1(add + n * n_in + k) : 0.f));
+  return make_uint2(r[0], r[1]);
+}
+
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+  const uint2 r = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
+}
+__device__ __forceinline__ void st4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void st4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+// One 32 x 32 block of a warp: lane L holds row L of the accumulator in v.
+template <typename TO>
+__device__ __forceinline__ void store_block(const WgradParams& p, float* stage, const float* v, int64_t row0, int64_t col0,
+                                            int lane) {
+  const TO* add = static_cast<const TO*>(p.add);
+  TO* out = static_cast<TO*>(p.out);
+  float4 a[8];
+  const int c = (lane & 7) * 4;
+  if (p.vec && add) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = row0 + i * 4 + (lane >> 3), col = col0 + c;
+      if (row < p.n_out && col < p.n_in) a[i] = ld4(add + row * p.n_in + col);
     }
+  }
+  __syncwarp();
+  float4* s = reinterpret_cast<float4*>(stage + lane * kEpiPitch);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  __syncwarp();
+  if (p.vec) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3);
+      const int64_t row = row0 + r, col = col0 + c;
+      if (row >= p.n_out || col >= p.n_in) continue;          // n_in % 4 == 0: the 4 columns are in range together
+      float4 d = *reinterpret_cast<const float4*>(stage + r * kEpiPitch + c);
+      if (add) {
+        d.x += a[i].x; d.y += a[i].y; d.z += a[i].z; d.w += a[i].w;
+      }
+      st4(out + row * p.n_in + col, d);
+    }
+  } else {
+    const int64_t col = col0 + lane;
+    if (col < p.n_in) {
+#pragma unroll 4
+      for (int r = 0; r < 32; ++r) {
+        const int64_t row = row0 + r;
+        if (row >= p.n_out) break;
+        float d = stage[r * kEpiPitch + lane];
+        if (add) d += load1(add + row * p.n_in + col);
+        store1(out + row * p.n_in + col, d);
+      }
+    }
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constant__ WgradParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const Smem sm = carve(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int unit = (int)(blockIdx.x >> 1);
+  const int tiles = p.tiles_m * p.tiles_n;
+  volatile int* abort = sm.abort;
+  int* status = p.status;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full_a[i], 1);
+      mbar_init(&sm.full_q[i], 1);
+      mbar_init(&sm.decoded[i], 2 * kDecWarps);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.tfull[i], 1);
+      mbar_init(&sm.tempty[i], 2 * kEpiWarps);
+    }
+    mbar_init(sm.drain, 1);
+    *sm.abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) tmem_alloc_pair(sm.tmem, kTmemCols);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *sm.tmem;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      tma_prefetch_desc(&p.dy);
+      tma_prefetch_desc(&p.q);
+      tma_prefetch_desc(&p.e);
+      uint32_t stage = 0, phase = 0, issued = 0, last_par = 0;
+      bool ok = true;
+      for (int t = unit; ok && t < tiles; t += p.units) {
+        int tm, tn;
+        tile_at(p, t, tm, tn);
+        const int a0 = tm * kTile + (int)rank * 128, b0 = tn * kTile + (int)rank * 128;
+        const int e0 = (b0 / kActBlock) & ~15;
+        for (int kb = 0; kb < p.nk; ++kb) {
+          if (!mbar_wait(&sm.empty[stage], phase ^ 1u, abort, status, kTimeoutNs)) {
+            ok = false;
+            break;
+          }
+          uint8_t* at = sm.stage + stage * kStageBytes;
+          // both CTAs' halves of dy complete on the even CTA's barrier; q stays here
+          const uint32_t fa = mapa_shared(smem_u32(&sm.full_a[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full_a[stage], 2 * kBytesA);
+          tma_load_3d_pair(at, &p.dy, fa, a0, kb * kDepth, 0);
+          tma_load_3d_pair(at + kBytesA / 2, &p.dy, fa, a0 + 64, kb * kDepth, 0);
+          mbar_arrive_expect_tx(&sm.full_q[stage], kBytesQ + kBytesE);
+          tma_load_3d(at + kBytesA + kBytesB, &p.q, &sm.full_q[stage], b0, kb * kDepth, 0);
+          tma_load_3d(at + kBytesA + kBytesB + kBytesQ, &p.e, &sm.full_q[stage], e0, kb * kDepth, 0);
+          issued |= 1u << stage;
+          last_par = (last_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // every issued copy must land before shared memory is given back
+      for (int s = 0; s < kStages; ++s)
+        if (issued & (1u << s)) {
+          mbar_wait(&sm.full_q[s], (last_par >> s) & 1u, nullptr, status, kTimeoutNs);
+          if (rank == 0) mbar_wait(&sm.full_a[s], (last_par >> s) & 1u, nullptr, status, kTimeoutNs);
+        }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32_bmn(kTile, kTile) | (1u << 15);   // both operands MN-major
+      const uint32_t base = smem_u32(sm.stage);
+      const uint64_t da0 = sdesc_mnmajor_sw128(base, kBytesA / 2, 1024);
+      const uint64_t db0 = sdesc_mnmajor_sw128(base + kBytesA, kBytesB / 2, 1024);
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = unit; ok && t < tiles; t += p.units) {
+        if (!mbar_wait(&sm.tempty[acc], acc_phase ^ 1u, abort, status, kTimeoutNs)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * (uint32_t)kTile;
+        for (int kb = 0; kb < p.nk; ++kb) {
+          if (!mbar_wait(&sm.full_a[stage], phase, abort, status, kTimeoutNs) ||
+              !mbar_wait_cluster(&sm.decoded[stage], phase, abort, status, kTimeoutNs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t off = stage * (uint32_t)(kStageBytes / 16);
+#pragma unroll
+          for (int s = 0; s < kDepth / 16; ++s)       // 16 tokens are 2048 bytes further in either operand
+            umma_bf16_pair(d, da0 + off + s * 128, db0 + off + s * 128, idesc, (kb | s) != 0 ? 1u : 0u);
+          umma_commit_pair(&sm.empty[stage], 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair(&sm.tfull[acc], 0x3);
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      umma_commit_pair(sm.drain, 0x1);
+      mbar_wait(sm.drain, 0, nullptr, status, kTimeoutNs);
+    }
+    __syncwarp();
+  } else if (warp < 2 + kEpiWarps) {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3;                        // the lanes of TMEM this warp may read
+    float* stage = sm.epi + (warp - 2) * (kEpiBytes / 4);
+    uint32_t acc = 0, acc_phase = 0;
+    for (int t = unit; t < tiles; t += p.units) {
+      int tm, tn;
+      tile_at(p, t, tm, tn);
+      const int64_t row0 = (int64_t)tm * kTile + rank * 128 + quad * 32;
+      const bool w = mbar_wait(&sm.tfull[acc], acc_phase, abort, status, kTimeoutNs);
+      if (!__all_sync(0xffffffffu, w)) break;
+      tc_fence_after();
+      const uint32_t from = tmem + acc * (uint32_t)kTile + ((uint32_t)(quad * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < kTile / 32; ++c) {
+        float v[32];
+        tmem_ld32(from + c * 32, v);
+        if (c == kTile / 32 - 1) {                    // read: the next tile's products may overwrite it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.tempty[acc]), 0));
+        }
+        const int64_t col0 = (int64_t)tn * kTile + c * 32;
+        if (row0 < p.n_out && col0 < p.n_in) {
+          if (p.out_f32) store_block<float>(p, stage, v, row0, col0, lane);
+          else store_block<__nv_bfloat16>(p, stage, v, row0, col0, lane);
+        }
+      }
+      acc ^= 1u;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  } else {
+    // ------------------------------------------------------------ decoders
+    const int dw = warp - 2 - kEpiWarps;              // 8 tokens of a step each
+    const int part = lane & 7;                        // 16 of the 128 columns
+    const int box = part >> 2;
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int t = unit; ok && t < tiles; t += p.units) {
+      int tm, tn;
+      tile_at(p, t, tm, tn);
+      const int e_at = (((tn * kTile + (int)rank * 128) / kActBlock) & 15) + (part >> 1);
+      for (int kb = 0; kb < p.nk; ++kb) {
+        const bool w = mbar_wait(&sm.full_q[stage], phase, abort, status, kTimeoutNs);
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
+        uint8_t* at = sm.stage + stage * kStageBytes;
+        const uint8_t* q = at + kBytesA + kBytesB;
+        const uint8_t* e = q + kBytesQ;
+        uint8_t* b = at + kBytesA + box * (kBytesB / 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int token = dw * 8 + i * 4 + (lane >> 3);
+          const uint4 w4 = *reinterpret_cast<const uint4*>(q + token * 128 + part * 16);
+          const uint32_t sb = e[token * 16 + e_at];
+          const uint32_t s1 = sb == 255u ? 0x7FC0u : sb << 7;          // 2^E in bf16
+          const uint32_t s2 = s1 | (s1 << 16);
+          const uint2 d0 = decode4(w4.x, s2), d1 = decode4(w4.y, s2), d2 = decode4(w4.z, s2), d3 = decode4(w4.w, s2);
+          // the two 16-byte chunks, swizzled by the token; lanes of the second box write their second
+          // chunk first, so that 8 lanes cover all banks
+          const int c0 = (part & 3) * 2;
+          const uint4 lo = make_uint4(d0.x, d0.y, d1.x, d1.y), hi = make_uint4(d2.x, d2.y, d3.x, d3.y);
+          uint8_t* row = b + token * 128;
+          const int sw = token & 7;
+          *reinterpret_cast<uint4*>(row + (((c0 + box) ^ sw) << 4)) = box ? hi : lo;
+          *reinterpret_cast<uint4*>(row + (((c0 + 1 - box) ^ sw) << 4)) = box ? lo : hi;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.decoded[stage]), 0));
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// out = add (or zero): the sum over no rows.
+template <typename TO>
+__global__ void __launch_bounds__(256) no_rows_kernel(const TO* add, TO* out, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    store1(out + i, add ? load1(add + i) : 0.f);
+}
+
+// Rows at any alignment to rows on 16-byte boundaries, as the tensor copies need them.
+__global__ void __launch_bounds__(256) align_rows_kernel(const __nv_bfloat16* __restrict__ src, int64_t ld, int64_t cols,
+                                                         __nv_bfloat16* __restrict__ dst, int64_t ld_dst, int64_t rows) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= cols) return;
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) dst[r * ld_dst + c] = src[r * ld + c];
 }
 
 constexpr int64_t kHeader = 256;
 
 bool sizes_ok(int64_t rows, int64_t n_out, int64_t n_in) {
   return rows >= 0 && n_out >= 1 && n_in >= 1 && rows < kMaxExtent && n_out < kMaxExtent / 2 && n_in < kMaxExtent / 2;
+}
+
+int64_t aligned_ld(int64_t n_out) { return round_up(n_out, 8); }
+
+// A rows x cols matrix of `type` (rows ld_bytes apart) in boxes of box_cols x 64 rows.
+bool encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t cols, int64_t rows, int64_t ld_bytes,
+                uint32_t box_cols, CUtensorMapSwizzle swizzle) {
+  const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld_bytes, (cuuint64_t)(ld_bytes * rows)};
+  const cuuint32_t box[3] = {box_cols, (cuuint32_t)kDepth, 1}, step[3] = {1, 1, 1};
+  return enc(map, type, 3, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTA pairs that are resident at once; 0 if the kernel cannot be set up.  Looked up once per device.
+int max_units() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (note_cuda_error(cudaGetDevice(&dev)) != cudaSuccess) return 0;
+  if (dev < 64 && known[dev].load() > 0) return known[dev].load();
+  if (note_cuda_error(cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)) != cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (note_cuda_error(cudaOccupancyMaxActiveClusters(&n, wgrad_kernel, &cfg)) != cudaSuccess || n < 1) return 0;
+  if (dev < 64) known[dev].store(n);
+  return n;
+}
+
+template <typename TO>
+int no_rows(const void* add, void* out, int64_t n, cudaStream_t s) {
+  const unsigned g = (unsigned)std::min<int64_t>(div_up(n, 256), 8 * (int64_t)sm_count());
+  return launch_kernel(no_rows_kernel<TO>, dim3(g), dim3(256), 0, s, 1, static_cast<const TO*>(add), static_cast<TO*>(out), n);
 }
 
 }  // namespace
@@ -60,7 +436,7 @@ using namespace cz;
 extern "C" int cz_act_wgrad_workspace(const void* dy, int64_t ld_dy, int64_t rows, int64_t n_out, int64_t n_in,
                                       size_t* bytes) {
   if (!bytes || !sizes_ok(rows, n_out, n_in) || !matrix_ok(dy, rows, n_out, ld_dy, 2)) return CZ_ERR_INVALID;
-  *bytes = kHeader;
+  *bytes = (size_t)(kHeader + (rows_aligned(dy, ld_dy, 2) ? 0 : rows * aligned_ld(n_out) * 2));
   return CZ_OK;
 }
 
@@ -73,19 +449,51 @@ extern "C" int cz_act_wgrad(const void* dy, int64_t ld_dy, const void* ckpt, int
   if (!is_dtype(out_dtype) || !out || !aligned(out, dtype_bytes(out_dtype)) || !aligned(add, dtype_bytes(out_dtype)) ||
       (!ckpt && rows > 0) || !aligned(ckpt, 16))
     return CZ_ERR_INVALID;
+  const int64_t tiles_m = div_up(n_out, kTile), tiles_n = div_up(n_in, kTile);
+  if (tiles_m * tiles_n > INT32_MAX / 2) return CZ_ERR_INVALID;
+  const uintptr_t o0 = reinterpret_cast<uintptr_t>(out), a0 = reinterpret_cast<uintptr_t>(add);
+  const uintptr_t span = (uintptr_t)(n_out * n_in * dtype_bytes(out_dtype));
+  if (add && a0 != o0 && a0 < o0 + span && o0 < a0 + span) return CZ_ERR_INVALID;   // part of add would be overwritten
   if (!workspace || workspace_bytes < need) return CZ_ERR_NOMEM;
   if (!aligned(workspace, 256)) return CZ_ERR_INVALID;
   const int st = check_sm103();
   if (st != CZ_OK) return st;
   NvtxRange range("cz/act_wgrad");
-  const dim3 grid((unsigned)div_up(n_in, kTile), (unsigned)div_up(n_out, kTile));
-  const ActLayout l = act_layout(rows, n_in);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(dy);
+  if (rows == 0)
+    return out_dtype == CZ_F32 ? no_rows<float>(add, out, n_out * n_in, s) : no_rows<__nv_bfloat16>(add, out, n_out * n_in, s);
+
+  if (!rows_aligned(dy, ld_dy, 2)) {
+    __nv_bfloat16* copy = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + kHeader);
+    const dim3 grid((unsigned)div_up(n_out, 256), (unsigned)std::min<int64_t>(rows, 4096));
+    const int r = launch_kernel(align_rows_kernel, grid, dim3(256), 0, s, 1, static_cast<const __nv_bfloat16*>(dy), ld_dy, n_out,
+                                copy, aligned_ld(n_out), rows);
+    if (r != CZ_OK) return r;
+    dy = copy;
+    ld_dy = aligned_ld(n_out);
+  }
+  const int units = max_units();
+  if (units == 0) return CZ_ERR_CUDA;
+  const ActLayout l = act_layout(rows, n_in);
   const uint8_t* ck = static_cast<const uint8_t*>(ckpt);
-  if (out_dtype == CZ_F32)
-    return launch_kernel(wgrad_kernel<float>, grid, kThreads, 0, s, 1, g, ld_dy, ck, l, rows, n_out, n_in,
-                         static_cast<const float*>(add), static_cast<float*>(out));
-  return launch_kernel(wgrad_kernel<__nv_bfloat16>, grid, kThreads, 0, s, 1, g, ld_dy, ck, l, rows, n_out, n_in,
-                       static_cast<const __nv_bfloat16*>(add), static_cast<__nv_bfloat16*>(out));
+  WgradParams p;
+  if (!encode_map(&p.dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, n_out, rows, ld_dy * 2, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, ck, l.ld_q, rows, l.ld_q, 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_map(&p.e, CU_TENSOR_MAP_DATA_TYPE_UINT8, ck + l.e_off, l.ld_e, rows, l.ld_e, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return CZ_ERR_CUDA;
+  p.add = add;
+  p.out = out;
+  p.status = static_cast<int32_t*>(workspace);
+  p.n_out = n_out;
+  p.n_in = n_in;
+  p.nk = (int32_t)div_up(rows, kDepth);
+  p.tiles_m = (int32_t)tiles_m;
+  p.tiles_n = (int32_t)tiles_n;
+  p.units = (int32_t)std::min<int64_t>(units, tiles_m * tiles_n);
+  p.out_f32 = out_dtype == CZ_F32;
+  // 4 elements at a time: 16 bytes of fp32, 8 of bf16
+  const uintptr_t b = (uintptr_t)dtype_bytes(out_dtype) * 4;
+  p.vec = n_in % 4 == 0 && aligned(out, b) && aligned(add, b);
+  // the cluster dimension is the kernel's own
+  return launch_kernel(wgrad_kernel, dim3((unsigned)(2 * p.units)), dim3(kThreads), kSmemBytes, s, 1, p);
 }

@@ -61,6 +61,9 @@ int muon_step(const cz_plan* plan, int32_t rank, float* flat_param, const void* 
 // reads and clears its status word.
 void* noalloc_scratch_if_set_up();
 
+// The driver's cuTensorMapEncodeTiled (12.0 interface), or null.
+void* tensor_map_encoder();
+
 // Keeps a CUDA error for cz_last_cuda_error of this thread; returns it.
 cudaError_t note_cuda_error(cudaError_t e);
 

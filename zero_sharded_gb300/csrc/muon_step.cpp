@@ -995,6 +995,8 @@ int get_internal_ws(size_t need, void** out, bool capturing) {
 
 }  // namespace
 
+void* tensor_map_encoder() { return reinterpret_cast<void*>(get_encode()); }
+
 cudaError_t note_cuda_error(cudaError_t e) { return note(e); }
 
 }  // namespace cz

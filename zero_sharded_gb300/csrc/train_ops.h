@@ -4,9 +4,9 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
-
 #include <utility>
 
 #include "cz_internal.h"
