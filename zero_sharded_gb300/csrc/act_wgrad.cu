@@ -31,17 +31,19 @@ namespace {
 
 constexpr int kTile = 256;                 // rows and columns of a pair's tile
 constexpr int kDepth = 64;                 // tokens a step
-constexpr int kStages = 5;
+constexpr int kStages = 6;                 // steps in flight from memory
+constexpr int kBufs = 3;                   // decoded steps
 constexpr int kBytesA = 128 * kDepth * 2, kBytesB = 128 * kDepth * 2, kBytesQ = 128 * kDepth, kBytesE = 16 * kDepth;
-constexpr int kStageBytes = kBytesA + kBytesB + kBytesQ + kBytesE;
+constexpr int kStageBytes = kBytesA + kBytesQ + kBytesE;
 constexpr int kEpiWarps = 4, kDecWarps = 8;
+constexpr int kDecGroups = 2, kGroupWarps = kDecWarps / kDecGroups;   // the groups take steps in turn
 constexpr int kThreads = 32 * (2 + kEpiWarps + kDecWarps);
 constexpr int kEpiPitch = 36;              // floats of a staged row: 16-byte accesses without bank conflicts
 constexpr int kEpiBytes = 32 * kEpiPitch * 4;
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kEpiBytes + 512;
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBufs * kBytesB + kEpiWarps * kEpiBytes + 512;
 constexpr uint32_t kTmemCols = 512;
 constexpr int64_t kTimeoutNs = 2000000000LL;
-static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
+static_assert(kStageBytes % 1024 == 0 && kBytesB % 1024 == 0, "swizzle atoms");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 struct WgradParams {
@@ -65,9 +67,10 @@ __device__ __forceinline__ void tile_at(const WgradParams& p, int t, int& tm, in
 }
 
 struct Smem {
-  uint8_t* stage;
+  uint8_t* stage;            // dy and q of the steps in flight
+  uint8_t* buf;              // decoded steps
   float* epi;
-  uint64_t *full_a, *full_q, *decoded, *empty, *tfull, *tempty, *drain;
+  uint64_t *full_a, *full_q, *empty_q, *done, *decoded, *tfull, *tempty, *drain;
   uint32_t* tmem;
   int* abort;
 };
@@ -77,14 +80,17 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
   uint8_t* p = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   s.stage = p;
   p += kStages * kStageBytes;
+  s.buf = p;
+  p += kBufs * kBytesB;
   s.epi = reinterpret_cast<float*>(p);
   p += kEpiWarps * kEpiBytes;
   uint64_t* b = reinterpret_cast<uint64_t*>(p);
   s.full_a = b;
   s.full_q = b + kStages;
-  s.decoded = b + 2 * kStages;
-  s.empty = b + 3 * kStages;
-  s.tfull = b + 4 * kStages;
+  s.empty_q = b + 2 * kStages;
+  s.done = b + 3 * kStages;
+  s.decoded = b + 4 * kStages;
+  s.tfull = s.decoded + kBufs;
   s.tempty = s.tfull + 2;
   s.drain = s.tempty + 2;
   s.tmem = reinterpret_cast<uint32_t*>(s.drain + 1);
@@ -175,9 +181,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.full_a[i], 1);
       mbar_init(&sm.full_q[i], 1);
-      mbar_init(&sm.decoded[i], 2 * kDecWarps);
-      mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.empty_q[i], kGroupWarps);
+      mbar_init(&sm.done[i], 1);
     }
+    for (int i = 0; i < kBufs; ++i) mbar_init(&sm.decoded[i], 2 * kGroupWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.tfull[i], 1);
       mbar_init(&sm.tempty[i], 2 * kEpiWarps);
@@ -207,7 +214,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
         const int a0 = tm * kTile + (int)rank * 128, b0 = tn * kTile + (int)rank * 128;
         const int e0 = (b0 / kActBlock) & ~15;
         for (int kb = 0; kb < p.nk; ++kb) {
-          if (!mbar_wait(&sm.empty[stage], phase ^ 1u, abort, status, kTimeoutNs)) {
+          // the products of the step that had this stage are done, and its q are read
+          if (!mbar_wait(&sm.done[stage], phase ^ 1u, abort, status, kTimeoutNs) ||
+              !mbar_wait(&sm.empty_q[stage], phase ^ 1u, abort, status, kTimeoutNs)) {
             ok = false;
             break;
           }
@@ -218,8 +227,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
           tma_load_3d_pair(at, &p.dy, fa, a0, kb * kDepth, 0);
           tma_load_3d_pair(at + kBytesA / 2, &p.dy, fa, a0 + 64, kb * kDepth, 0);
           mbar_arrive_expect_tx(&sm.full_q[stage], kBytesQ + kBytesE);
-          tma_load_3d(at + kBytesA + kBytesB, &p.q, &sm.full_q[stage], b0, kb * kDepth, 0);
-          tma_load_3d(at + kBytesA + kBytesB + kBytesQ, &p.e, &sm.full_q[stage], e0, kb * kDepth, 0);
+          tma_load_3d(at + kBytesA, &p.q, &sm.full_q[stage], b0, kb * kDepth, 0);
+          tma_load_3d(at + kBytesA + kBytesQ, &p.e, &sm.full_q[stage], e0, kb * kDepth, 0);
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) {
@@ -242,8 +251,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
       constexpr uint32_t idesc = idesc_bf16_f32_bmn(kTile, kTile) | (1u << 15);   // both operands MN-major
       const uint32_t base = smem_u32(sm.stage);
       const uint64_t da0 = sdesc_mnmajor_sw128(base, kBytesA / 2, 1024);
-      const uint64_t db0 = sdesc_mnmajor_sw128(base + kBytesA, kBytesB / 2, 1024);
-      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      const uint64_t db0 = sdesc_mnmajor_sw128(smem_u32(sm.buf), kBytesB / 2, 1024);
+      uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
       for (int t = unit; ok && t < tiles; t += p.units) {
         if (!mbar_wait(&sm.tempty[acc], acc_phase ^ 1u, abort, status, kTimeoutNs)) break;
@@ -251,19 +260,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
         const uint32_t d = tmem + acc * (uint32_t)kTile;
         for (int kb = 0; kb < p.nk; ++kb) {
           if (!mbar_wait(&sm.full_a[stage], phase, abort, status, kTimeoutNs) ||
-              !mbar_wait_cluster(&sm.decoded[stage], phase, abort, status, kTimeoutNs)) {
+              !mbar_wait_cluster(&sm.decoded[buf], buf_phase, abort, status, kTimeoutNs)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t off = stage * (uint32_t)(kStageBytes / 16);
+          const uint64_t da = da0 + stage * (uint32_t)(kStageBytes / 16), db = db0 + buf * (uint32_t)(kBytesB / 16);
 #pragma unroll
           for (int s = 0; s < kDepth / 16; ++s)       // 16 tokens are 2048 bytes further in either operand
-            umma_bf16_pair(d, da0 + off + s * 128, db0 + off + s * 128, idesc, (kb | s) != 0 ? 1u : 0u);
-          umma_commit_pair(&sm.empty[stage], 0x3);
+            umma_bf16_pair(d, da + s * 128, db + s * 128, idesc, (kb | s) != 0 ? 1u : 0u);
+          umma_commit_pair(&sm.done[stage], 0x3);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
+          }
+          if (++buf == kBufs) {
+            buf = 0;
+            buf_phase ^= 1u;
           }
         }
         if (!ok) break;
@@ -308,33 +321,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
     }
   } else {
     // ------------------------------------------------------------ decoders
-    const int dw = warp - 2 - kEpiWarps;              // 8 tokens of a step each
+    const int dw = warp - 2 - kEpiWarps, group = dw / kGroupWarps;
+    constexpr int kIter = kDepth / 4 / kGroupWarps;   // 4 tokens a warp each time
+    const int token0 = (dw % kGroupWarps) * (4 * kIter) + (lane >> 3);
     const int part = lane & 7;                        // 16 of the 128 columns
     const int box = part >> 2;
-    uint32_t stage = 0, phase = 0;
+    int step = 0;                                     // of all tiles
     bool ok = true;
     for (int t = unit; ok && t < tiles; t += p.units) {
       int tm, tn;
       tile_at(p, t, tm, tn);
       const int e_at = (((tn * kTile + (int)rank * 128) / kActBlock) & 15) + (part >> 1);
-      for (int kb = 0; kb < p.nk; ++kb) {
-        const bool w = mbar_wait(&sm.full_q[stage], phase, abort, status, kTimeoutNs);
+      for (int kb = 0; kb < p.nk; ++kb, ++step) {
+        if (step % kDecGroups != group) continue;
+        const int stage = step % kStages;
+        bool w = mbar_wait(&sm.full_q[stage], (uint32_t)(step / kStages) & 1u, abort, status, kTimeoutNs);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
         }
-        uint8_t* at = sm.stage + stage * kStageBytes;
-        const uint8_t* q = at + kBytesA + kBytesB;
+        const uint8_t* q = sm.stage + stage * kStageBytes + kBytesA;
         const uint8_t* e = q + kBytesQ;
-        uint8_t* b = at + kBytesA + box * (kBytesB / 2);
+        uint4 raw[kIter];
+        uint32_t sb[kIter];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int token = dw * 8 + i * 4 + (lane >> 3);
-          const uint4 w4 = *reinterpret_cast<const uint4*>(q + token * 128 + part * 16);
-          const uint32_t sb = e[token * 16 + e_at];
-          const uint32_t s1 = sb == 255u ? 0x7FC0u : sb << 7;          // 2^E in bf16
+        for (int i = 0; i < kIter; ++i) {
+          raw[i] = *reinterpret_cast<const uint4*>(q + (token0 + 4 * i) * 128 + part * 16);
+          sb[i] = e[(token0 + 4 * i) * 16 + e_at];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.empty_q[stage]);
+        // the buffer: the products of the step that had it, kBufs ago, are done
+        if (step >= kBufs) {
+          const int last = step - kBufs;
+          w = mbar_wait(&sm.done[last % kStages], (uint32_t)(last / kStages) & 1u, abort, status, kTimeoutNs);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+        }
+        const int buf = step % kBufs;
+        uint8_t* b = sm.buf + buf * kBytesB + box * (kBytesB / 2);
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          const int token = token0 + 4 * i;
+          const uint32_t s1 = sb[i] == 255u ? 0x7FC0u : sb[i] << 7;    // 2^E in bf16
           const uint32_t s2 = s1 | (s1 << 16);
-          const uint2 d0 = decode4(w4.x, s2), d1 = decode4(w4.y, s2), d2 = decode4(w4.z, s2), d3 = decode4(w4.w, s2);
+          const uint2 d0 = decode4(raw[i].x, s2), d1 = decode4(raw[i].y, s2), d2 = decode4(raw[i].z, s2),
+                      d3 = decode4(raw[i].w, s2);
           // the two 16-byte chunks, swizzled by the token; lanes of the second box write their second
           // chunk first, so that 8 lanes cover all banks
           const int c0 = (part & 3) * 2;
@@ -346,11 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.decoded[stage]), 0));
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.decoded[buf]), 0));
       }
     }
   }
