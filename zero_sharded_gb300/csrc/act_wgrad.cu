@@ -6,12 +6,13 @@
 // Both operands lie with their outer dimension contiguous (the sum runs over rows), so both are
 // MN-major in shared memory.  A CTA pair (cta_group::2) computes a 256 x 256 tile of out in steps of
 // 64 tokens; each CTA holds 128 columns of dy and 128 of x^ a step and receives 128 rows of the tile.  Per CTA:
-//   warp 0       TMA producer: dy (128-byte swizzle), q and its scale bytes, a ring of stages
+//   warp 0       TMA producer of dy (128-byte swizzle)
 //   warp 1       TMEM allocation (two 256-column accumulators) and, in the even CTA, the thread that
 //                issues tcgen05.mma
-//   warps 2-5    epilogue: tcgen05.ld, 32 x 32 blocks through shared memory so that rows of out are
+//   warp 2       TMA producer of q, which runs ahead by itself
+//   warps 3-6    epilogue: tcgen05.ld, 32 x 32 blocks through shared memory so that rows of out are
 //                read (add) and written 128 bytes at a time
-//   warps 6-13   decoders: 16 q at a time from shared memory to swizzled bf16 in the stage
+//   warps 7-14   decoders: 16 q at a time from shared memory to swizzled bf16 in the stage
 // A byte q becomes bf16 without integer conversion: 0x4300 | (q & 127) is 128 + (q & 127), 0x4300 | (q & 128)
 // is 128 or 256, and their difference is q (exact); one more multiplication applies 2^E (exact).
 // Per pair of elements: a byte permutation, two masks, a difference and a product.
@@ -31,19 +32,28 @@ namespace {
 
 constexpr int kTile = 256;                 // rows and columns of a pair's tile
 constexpr int kDepth = 64;                 // tokens a step
-constexpr int kStages = 6;                 // steps in flight from memory
-constexpr int kBufs = 3;                   // decoded steps
+#ifndef CFG_A
+#define CFG_A 5
+#define CFG_Q 5
+#define CFG_B 5
+#define CFG_G 2
+#define CFG_W 8
+#endif
+constexpr int kStages = CFG_A;                 // steps of dy in flight
+constexpr int kStagesQ = CFG_Q;                // steps of q in flight
+constexpr int kBufs = CFG_B;                   // decoded steps
 constexpr int kBytesA = 128 * kDepth * 2, kBytesB = 128 * kDepth * 2, kBytesQ = 128 * kDepth, kBytesE = 16 * kDepth;
-constexpr int kStageBytes = kBytesA + kBytesQ + kBytesE;
-constexpr int kEpiWarps = 4, kDecWarps = 8;
-constexpr int kDecGroups = 2, kGroupWarps = kDecWarps / kDecGroups;   // the groups take steps in turn
-constexpr int kThreads = 32 * (2 + kEpiWarps + kDecWarps);
+constexpr int kBytesQE = kBytesQ + kBytesE;
+constexpr int kEpiWarps = 4, kDecWarps = CFG_W;
+constexpr int kDecGroups = CFG_G, kGroupWarps = kDecWarps / kDecGroups;   // the groups take steps in turn
+constexpr int kFirstDec = 3 + kEpiWarps;
+constexpr int kThreads = 32 * (kFirstDec + kDecWarps);
 constexpr int kEpiPitch = 36;              // floats of a staged row: 16-byte accesses without bank conflicts
 constexpr int kEpiBytes = 32 * kEpiPitch * 4;
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBufs * kBytesB + kEpiWarps * kEpiBytes + 512;
+constexpr int kSmemBytes = 1024 + kStages * kBytesA + kBufs * kBytesB + kStagesQ * kBytesQE + kEpiWarps * kEpiBytes + 512;
 constexpr uint32_t kTmemCols = 512;
-constexpr int64_t kTimeoutNs = 2000000000LL;
-static_assert(kStageBytes % 1024 == 0 && kBytesB % 1024 == 0, "swizzle atoms");
+constexpr int64_t kTimeoutClocks = 4000000000LL;   // about 2 s
+static_assert(kBytesA % 1024 == 0 && kBytesB % 1024 == 0 && kBytesQE % 128 == 0, "swizzle atoms");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 struct WgradParams {
@@ -67,10 +77,11 @@ __device__ __forceinline__ void tile_at(const WgradParams& p, int t, int& tm, in
 }
 
 struct Smem {
-  uint8_t* stage;            // dy and q of the steps in flight
+  uint8_t* a;                // dy of the steps in flight
   uint8_t* buf;              // decoded steps
+  uint8_t* q;                // q and scale bytes of the steps in flight
   float* epi;
-  uint64_t *full_a, *full_q, *empty_q, *done, *decoded, *tfull, *tempty, *drain;
+  uint64_t *full_a, *done_a, *full_q, *empty_q, *decoded, *done_b, *tfull, *tempty, *drain;
   uint32_t* tmem;
   int* abort;
 };
@@ -78,19 +89,22 @@ struct Smem {
 __device__ __forceinline__ Smem carve(uint8_t* raw) {
   Smem s;
   uint8_t* p = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  s.stage = p;
-  p += kStages * kStageBytes;
+  s.a = p;
+  p += kStages * kBytesA;
   s.buf = p;
   p += kBufs * kBytesB;
+  s.q = p;
+  p += kStagesQ * kBytesQE;
   s.epi = reinterpret_cast<float*>(p);
   p += kEpiWarps * kEpiBytes;
   uint64_t* b = reinterpret_cast<uint64_t*>(p);
   s.full_a = b;
-  s.full_q = b + kStages;
-  s.empty_q = b + 2 * kStages;
-  s.done = b + 3 * kStages;
-  s.decoded = b + 4 * kStages;
-  s.tfull = s.decoded + kBufs;
+  s.done_a = s.full_a + kStages;
+  s.full_q = s.done_a + kStages;
+  s.empty_q = s.full_q + kStagesQ;
+  s.decoded = s.empty_q + kStagesQ;
+  s.done_b = s.decoded + kBufs;
+  s.tfull = s.done_b + kBufs;
   s.tempty = s.tfull + 2;
   s.drain = s.tempty + 2;
   s.tmem = reinterpret_cast<uint32_t*>(s.drain + 1);
@@ -180,11 +194,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.full_a[i], 1);
+      mbar_init(&sm.done_a[i], 1);
+    }
+    for (int i = 0; i < kStagesQ; ++i) {
       mbar_init(&sm.full_q[i], 1);
       mbar_init(&sm.empty_q[i], kGroupWarps);
-      mbar_init(&sm.done[i], 1);
     }
-    for (int i = 0; i < kBufs; ++i) mbar_init(&sm.decoded[i], 2 * kGroupWarps);
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(&sm.decoded[i], 2 * kGroupWarps);
+      mbar_init(&sm.done_b[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.tfull[i], 1);
       mbar_init(&sm.tempty[i], 2 * kEpiWarps);
@@ -200,13 +219,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
   tc_fence_after();
   const uint32_t tmem = *sm.tmem;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ TMA producers: dy (warp 0), q (warp 2)
     if (lane == 0) {
-      tma_prefetch_desc(&p.dy);
-      tma_prefetch_desc(&p.q);
-      tma_prefetch_desc(&p.e);
-      uint32_t stage = 0, phase = 0, issued = 0, last_par = 0;
+      const bool is_q = warp == 2;
+      const int stages = is_q ? kStagesQ : kStages;
+      uint64_t* full = is_q ? sm.full_q : sm.full_a;
+      uint64_t* freed = is_q ? sm.empty_q : sm.done_a;
+      tma_prefetch_desc(is_q ? &p.q : &p.dy);
+      if (is_q) tma_prefetch_desc(&p.e);
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, last_par = 0;
       bool ok = true;
       for (int t = unit; ok && t < tiles; t += p.units) {
         int tm, tn;
@@ -214,62 +237,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
         const int a0 = tm * kTile + (int)rank * 128, b0 = tn * kTile + (int)rank * 128;
         const int e0 = (b0 / kActBlock) & ~15;
         for (int kb = 0; kb < p.nk; ++kb) {
-          // the products of the step that had this stage are done, and its q are read
-          if (!mbar_wait(&sm.done[stage], phase ^ 1u, abort, status, kTimeoutNs) ||
-              !mbar_wait(&sm.empty_q[stage], phase ^ 1u, abort, status, kTimeoutNs)) {
+          if (!mbar_poll(&freed[stage], phase ^ 1u, abort, status, kTimeoutClocks)) {
             ok = false;
             break;
           }
-          uint8_t* at = sm.stage + stage * kStageBytes;
-          // both CTAs' halves of dy complete on the even CTA's barrier; q stays here
-          const uint32_t fa = mapa_shared(smem_u32(&sm.full_a[stage]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&sm.full_a[stage], 2 * kBytesA);
-          tma_load_3d_pair(at, &p.dy, fa, a0, kb * kDepth, 0);
-          tma_load_3d_pair(at + kBytesA / 2, &p.dy, fa, a0 + 64, kb * kDepth, 0);
-          mbar_arrive_expect_tx(&sm.full_q[stage], kBytesQ + kBytesE);
-          tma_load_3d(at + kBytesA, &p.q, &sm.full_q[stage], b0, kb * kDepth, 0);
-          tma_load_3d(at + kBytesA + kBytesQ, &p.e, &sm.full_q[stage], e0, kb * kDepth, 0);
+          if (is_q) {
+            uint8_t* at = sm.q + stage * kBytesQE;
+            mbar_arrive_expect_tx(&full[stage], kBytesQE);
+            tma_load_3d(at, &p.q, &full[stage], b0, kb * kDepth, 0);
+            tma_load_3d(at + kBytesQ, &p.e, &full[stage], e0, kb * kDepth, 0);
+          } else {
+            // both CTAs' halves of dy complete on the even CTA's barrier
+            uint8_t* at = sm.a + stage * kBytesA;
+            const uint32_t fa = mapa_shared(smem_u32(&full[stage]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kBytesA);
+            tma_load_3d_pair(at, &p.dy, fa, a0, kb * kDepth, 0);
+            tma_load_3d_pair(at + kBytesA / 2, &p.dy, fa, a0 + 64, kb * kDepth, 0);
+          }
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      // every issued copy must land before shared memory is given back
-      for (int s = 0; s < kStages; ++s)
-        if (issued & (1u << s)) {
-          mbar_wait(&sm.full_q[s], (last_par >> s) & 1u, nullptr, status, kTimeoutNs);
-          if (rank == 0) mbar_wait(&sm.full_a[s], (last_par >> s) & 1u, nullptr, status, kTimeoutNs);
-        }
+      // every issued copy must land before shared memory is given back (the odd CTA's dy is
+      // counted in the even one, for which it waits at the end)
+      for (int s = 0; s < stages; ++s)
+        if ((issued & (1u << s)) && (is_q || rank == 0))
+          mbar_poll(&full[s], (last_par >> s) & 1u, nullptr, status, kTimeoutClocks);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (rank == 0 && lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32_bmn(kTile, kTile) | (1u << 15);   // both operands MN-major
-      const uint32_t base = smem_u32(sm.stage);
-      const uint64_t da0 = sdesc_mnmajor_sw128(base, kBytesA / 2, 1024);
+      const uint64_t da0 = sdesc_mnmajor_sw128(smem_u32(sm.a), kBytesA / 2, 1024);
       const uint64_t db0 = sdesc_mnmajor_sw128(smem_u32(sm.buf), kBytesB / 2, 1024);
       uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
       for (int t = unit; ok && t < tiles; t += p.units) {
-        if (!mbar_wait(&sm.tempty[acc], acc_phase ^ 1u, abort, status, kTimeoutNs)) break;
+        if (!mbar_poll(&sm.tempty[acc], acc_phase ^ 1u, abort, status, kTimeoutClocks)) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * (uint32_t)kTile;
         for (int kb = 0; kb < p.nk; ++kb) {
-          if (!mbar_wait(&sm.full_a[stage], phase, abort, status, kTimeoutNs) ||
-              !mbar_wait_cluster(&sm.decoded[buf], buf_phase, abort, status, kTimeoutNs)) {
+          if (!mbar_poll(&sm.full_a[stage], phase, abort, status, kTimeoutClocks) ||
+              !mbar_poll<true>(&sm.decoded[buf], buf_phase, abort, status, kTimeoutClocks)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t da = da0 + stage * (uint32_t)(kStageBytes / 16), db = db0 + buf * (uint32_t)(kBytesB / 16);
+          const uint64_t da = da0 + stage * (uint32_t)(kBytesA / 16), db = db0 + buf * (uint32_t)(kBytesB / 16);
 #pragma unroll
           for (int s = 0; s < kDepth / 16; ++s)       // 16 tokens are 2048 bytes further in either operand
             umma_bf16_pair(d, da + s * 128, db + s * 128, idesc, (kb | s) != 0 ? 1u : 0u);
-          umma_commit_pair(&sm.done[stage], 0x3);
+          umma_commit_pair(&sm.done_a[stage], 0x3);
+          umma_commit_pair(&sm.done_b[buf], 0x3);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
@@ -285,19 +309,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
         if (acc == 0) acc_phase ^= 1u;
       }
       umma_commit_pair(sm.drain, 0x1);
-      mbar_wait(sm.drain, 0, nullptr, status, kTimeoutNs);
+      mbar_poll(sm.drain, 0, nullptr, status, kTimeoutClocks);
     }
     __syncwarp();
-  } else if (warp < 2 + kEpiWarps) {
+  } else if (warp < kFirstDec) {
     // ------------------------------------------------------------ epilogue
     const int quad = warp & 3;                        // the lanes of TMEM this warp may read
-    float* stage = sm.epi + (warp - 2) * (kEpiBytes / 4);
+    float* stage = sm.epi + (warp - 3) * (kEpiBytes / 4);
     uint32_t acc = 0, acc_phase = 0;
     for (int t = unit; t < tiles; t += p.units) {
       int tm, tn;
       tile_at(p, t, tm, tn);
       const int64_t row0 = (int64_t)tm * kTile + rank * 128 + quad * 32;
-      const bool w = mbar_wait(&sm.tfull[acc], acc_phase, abort, status, kTimeoutNs);
+      const bool w = mbar_poll(&sm.tfull[acc], acc_phase, abort, status, kTimeoutClocks);
       if (!__all_sync(0xffffffffu, w)) break;
       tc_fence_after();
       const uint32_t from = tmem + acc * (uint32_t)kTile + ((uint32_t)(quad * 32) << 16);
@@ -321,7 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
     }
   } else {
     // ------------------------------------------------------------ decoders
-    const int dw = warp - 2 - kEpiWarps, group = dw / kGroupWarps;
+    const int dw = warp - kFirstDec, group = dw / kGroupWarps;
     constexpr int kIter = kDepth / 4 / kGroupWarps;   // 4 tokens a warp each time
     const int token0 = (dw % kGroupWarps) * (4 * kIter) + (lane >> 3);
     const int part = lane & 7;                        // 16 of the 128 columns
@@ -334,13 +358,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
       const int e_at = (((tn * kTile + (int)rank * 128) / kActBlock) & 15) + (part >> 1);
       for (int kb = 0; kb < p.nk; ++kb, ++step) {
         if (step % kDecGroups != group) continue;
-        const int stage = step % kStages;
-        bool w = mbar_wait(&sm.full_q[stage], (uint32_t)(step / kStages) & 1u, abort, status, kTimeoutNs);
+        const int stage = step % kStagesQ;
+        bool w = mbar_poll(&sm.full_q[stage], (uint32_t)(step / kStagesQ) & 1u, abort, status, kTimeoutClocks);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
         }
-        const uint8_t* q = sm.stage + stage * kStageBytes + kBytesA;
+        const uint8_t* q = sm.q + stage * kBytesQE;
         const uint8_t* e = q + kBytesQ;
         uint4 raw[kIter];
         uint32_t sb[kIter];
@@ -351,16 +375,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty_q[stage]);
-        // the buffer: the products of the step that had it, kBufs ago, are done
-        if (step >= kBufs) {
-          const int last = step - kBufs;
-          w = mbar_wait(&sm.done[last % kStages], (uint32_t)(last / kStages) & 1u, abort, status, kTimeoutNs);
-          if (!__all_sync(0xffffffffu, w)) {
-            ok = false;
-            break;
-          }
-        }
+        // the products that read the buffer last are done
         const int buf = step % kBufs;
+        w = mbar_poll(&sm.done_b[buf], ((uint32_t)(step / kBufs) & 1u) ^ 1u, abort, status, kTimeoutClocks);
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
         uint8_t* b = sm.buf + buf * kBytesB + box * (kBytesB / 2);
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
@@ -380,7 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.decoded[buf]), 0));
+        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&sm.decoded[buf]), 0));
       }
     }
   }

@@ -118,15 +118,19 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
-                                                  int64_t timeout_ns) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((it & 255u) == 0) {
+// As mbar_wait, for waits that block in every step of a chain: the bound is read from the SM's
+// own clock, and only after some polls (%globaltimer costs most of a microsecond).
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
+                                          int64_t clocks) {
+  int64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if ((it & 255u) == 255u) {
       if (abort && *abort) return false;
-      if ((int64_t)(globaltimer_ns() - t0) > timeout_ns) {
+      const int64_t now = clock64();
+      if (it == 255u) t0 = now;
+      else if (now - t0 > clocks) {
         record_status(status, CZ_ERR_TIMEOUT);
         if (abort) *abort = 1;
         return false;
@@ -223,6 +227,12 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// The same with the default (CTA) scope, for handing over data that stays in this SM's shared memory,
+// was ordered for the async proxy by fence.proxy.async, and is read by this SM's own tensor core: only
+// the count has to travel.  The cluster-scope release above costs over half a microsecond.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // TMA load into this CTA's smem whose completion is signalled on an mbarrier
 // that may live in the peer CTA of the pair (cluster address).
