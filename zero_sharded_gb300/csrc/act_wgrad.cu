@@ -3,19 +3,23 @@
 // on the 5th-generation tensor cores.  x^ is exact in bf16, so the product is bf16 x bf16 with
 // fp32 sums, and reading 33/32 bytes an element in place of 2 only adds the decoding.
 //
-// Both operands lie with their outer dimension contiguous (the sum runs over rows), so both are
-// MN-major in shared memory.  A CTA pair (cta_group::2) computes a 256 x 256 tile of out in steps of
-// 64 tokens; each CTA holds 128 columns of dy and 128 of x^ a step and receives 128 rows of the tile.  Per CTA:
+// The tile computed is out^T: M = 256 columns k of out, N = 256 rows n, a CTA pair (cta_group::2) a tile, in
+// steps of 64 tokens.  x^ is the A operand and goes from registers to TMEM: through shared memory
+// the decoded values would be written and read again there, and with the copies and the dy operand
+// that is 81 KB a step and SM, 633 clocks at 128 bytes a clock against the 512 of the products (measured:
+// 1.69 ms for 8192 x 25600 x 5120); this way it is 49 KB.  dy is the B operand, MN-major (the sum runs over
+// its rows).  TMEM: 256 columns of accumulator, 8 x 32 of decoded steps.  Lanes of the accumulator run along k, so
+// the epilogue reads add and writes out 128 bytes a warp without staging; it takes the whole
+// accumulator into registers first, and the next tile's products start.  Per CTA:
 //   warp 0       TMA producer of dy (128-byte swizzle)
-//   warp 1       TMEM allocation (two 256-column accumulators) and, in the even CTA, the thread that
-//                issues tcgen05.mma
-//   warp 2       TMA producer of q, which runs ahead by itself
-//   warps 3-6    epilogue: tcgen05.ld, 32 x 32 blocks through shared memory so that rows of out are
-//                read (add) and written 128 bytes at a time
-//   warps 7-14   decoders: 16 q at a time from shared memory to swizzled bf16 in the stage
-// A byte q becomes bf16 without integer conversion: 0x4300 | (q & 127) is 128 + (q & 127), 0x4300 | (q & 128)
-// is 128 or 256, and their difference is q (exact); one more multiplication applies 2^E (exact).
-// Per pair of elements: a byte permutation, two masks, a difference and a product.
+//   warp 1       TMEM allocation and, in the even CTA, the thread that issues tcgen05.mma
+//   warp 2       TMA producer of q and its scale bytes, which runs ahead by itself
+//   warps 4-11   epilogue, two a quarter of the lanes
+//   warps 12-19  decoders: two groups of four warps take steps in turn
+// A decoder transposes 16 x 16 bytes with ldmatrix, which leaves 4 tokens of one column in a
+// register, and a byte q becomes bf16 without integer conversion: 0x4300 | (q & 127) is 128 + (q & 127),
+// 0x4300 | (q & 128) is 128 or 256, and their difference is q (exact); one more multiplication
+// applies 2^E (exact).  Per pair of elements: a byte permutation, two masks, a difference and a product.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -32,29 +36,23 @@ namespace {
 
 constexpr int kTile = 256;                 // rows and columns of a pair's tile
 constexpr int kDepth = 64;                 // tokens a step
-#ifndef CFG_A
-#define CFG_A 5
-#define CFG_Q 5
-#define CFG_B 5
-#define CFG_G 2
-#define CFG_W 8
-#endif
-constexpr int kStages = CFG_A;                 // steps of dy in flight
-constexpr int kStagesQ = CFG_Q;                // steps of q in flight
-constexpr int kBufs = CFG_B;                   // decoded steps
-constexpr int kBytesA = 128 * kDepth * 2, kBytesB = 128 * kDepth * 2, kBytesQ = 128 * kDepth, kBytesE = 16 * kDepth;
+constexpr int kStages = 8;                 // steps in flight: dy and q in shared memory, decoded in TMEM
+constexpr int kBytesB = 128 * kDepth * 2, kBytesQ = 128 * kDepth, kBytesE = 16 * kDepth;
 constexpr int kBytesQE = kBytesQ + kBytesE;
-constexpr int kEpiWarps = 4, kDecWarps = CFG_W;
-constexpr int kDecGroups = CFG_G, kGroupWarps = kDecWarps / kDecGroups;   // the groups take steps in turn
-constexpr int kFirstDec = 3 + kEpiWarps;
+constexpr int kEpiWarps = 8, kDecWarps = 8;
+constexpr int kDecGroups = 2, kGroupWarps = kDecWarps / kDecGroups;   // the groups take steps in turn
+constexpr int kFirstEpi = 4, kFirstDec = kFirstEpi + kEpiWarps;
 constexpr int kThreads = 32 * (kFirstDec + kDecWarps);
-constexpr int kEpiPitch = 36;              // floats of a staged row: 16-byte accesses without bank conflicts
-constexpr int kEpiBytes = 32 * kEpiPitch * 4;
-constexpr int kSmemBytes = 1024 + kStages * kBytesA + kBufs * kBytesB + kStagesQ * kBytesQE + kEpiWarps * kEpiBytes + 512;
-constexpr uint32_t kTmemCols = 512;
+// Registers: 96 a thread at launch, 640 x 96 = 61440; then 128 x 48 + 256 x 152 + 256 x 64 = 61440.
+constexpr int kRegsFew = 48, kRegsEpi = 152, kRegsDec = 64;
+static_assert(128 * kRegsFew + 32 * kEpiWarps * kRegsEpi + 32 * kDecWarps * kRegsDec <= kThreads * 96, "register split");
+constexpr int kScaleBytes = 2 * kDepth;    // a decoder warp's scales of a step, bf16
+constexpr int kSmemBytes = 1024 + kStages * (kBytesB + kBytesQE) + kDecWarps * kScaleBytes + 512;
+constexpr uint32_t kTmemCols = 512, kTmemA = 256, kTmemStep = kDepth / 2;
 constexpr int64_t kTimeoutClocks = 4000000000LL;   // about 2 s
-static_assert(kBytesA % 1024 == 0 && kBytesB % 1024 == 0 && kBytesQE % 128 == 0, "swizzle atoms");
+static_assert(kBytesB % 1024 == 0 && kBytesQ % 1024 == 0, "swizzle atoms");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+static_assert(kTmemA + kStages * kTmemStep <= kTmemCols, "tensor memory");
 
 struct WgradParams {
   CUtensorMap dy, q, e;
@@ -65,7 +63,7 @@ struct WgradParams {
   int32_t nk;                // steps of a whole tile
   int32_t tiles_m, tiles_n;  // tiles over n_out and n_in
   int32_t units;             // CTA pairs
-  int32_t out_f32, vec;      // vec: rows of out and add can be accessed 16 bytes at a time
+  int32_t out_f32;
 };
 
 // Tile t of the raster: groups of 8 tile rows, so that the tiles in flight share few panels of either operand.
@@ -77,11 +75,11 @@ __device__ __forceinline__ void tile_at(const WgradParams& p, int t, int& tm, in
 }
 
 struct Smem {
-  uint8_t* a;                // dy of the steps in flight
-  uint8_t* buf;              // decoded steps
-  uint8_t* q;                // q and scale bytes of the steps in flight
-  float* epi;
-  uint64_t *full_a, *done_a, *full_q, *empty_q, *decoded, *done_b, *tfull, *tempty, *drain;
+  uint8_t* b;                // dy of the steps in flight
+  uint8_t* q;                // q of the steps in flight
+  uint8_t* e;                // their scale bytes
+  uint16_t* scales;
+  uint64_t *full_b, *done, *full_q, *empty_q, *decoded, *tfull, *tempty, *drain;
   uint32_t* tmem;
   int* abort;
 };
@@ -89,96 +87,107 @@ struct Smem {
 __device__ __forceinline__ Smem carve(uint8_t* raw) {
   Smem s;
   uint8_t* p = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  s.a = p;
-  p += kStages * kBytesA;
-  s.buf = p;
-  p += kBufs * kBytesB;
+  s.b = p;
+  p += kStages * kBytesB;
   s.q = p;
-  p += kStagesQ * kBytesQE;
-  s.epi = reinterpret_cast<float*>(p);
-  p += kEpiWarps * kEpiBytes;
+  p += kStages * kBytesQ;
+  s.e = p;
+  p += kStages * kBytesE;
+  s.scales = reinterpret_cast<uint16_t*>(p);
+  p += kDecWarps * kScaleBytes;
   uint64_t* b = reinterpret_cast<uint64_t*>(p);
-  s.full_a = b;
-  s.done_a = s.full_a + kStages;
-  s.full_q = s.done_a + kStages;
-  s.empty_q = s.full_q + kStagesQ;
-  s.decoded = s.empty_q + kStagesQ;
-  s.done_b = s.decoded + kBufs;
-  s.tfull = s.done_b + kBufs;
-  s.tempty = s.tfull + 2;
-  s.drain = s.tempty + 2;
+  s.full_b = b;
+  s.done = s.full_b + kStages;
+  s.full_q = s.done + kStages;
+  s.empty_q = s.full_q + kStages;
+  s.decoded = s.empty_q + kStages;
+  s.tfull = s.decoded + kStages;
+  s.tempty = s.tfull + 1;
+  s.drain = s.tempty + 1;
   s.tmem = reinterpret_cast<uint32_t*>(s.drain + 1);
   s.abort = reinterpret_cast<int*>(s.drain + 2);
   return s;
 }
 
-// 4 q bytes to 4 bf16 values q * s.
-__device__ __forceinline__ uint2 decode4(uint32_t w, uint32_t scale2) {
+// 4 q bytes (consecutive tokens) to 4 bf16 values q * s, the scales of the first and second two tokens packed.
+__device__ __forceinline__ uint2 decode4(uint32_t w, uint2 scale) {
   uint32_t r[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t p = __byte_perm(w, 0x43434343u, h ? 0x4342 : 0x4140);
     const uint32_t a = p & 0xFF7FFF7Fu, b = p & 0xFF80FF80u;
-    asm("{\n\t.reg .b32 d;\n\tsub.rn.bf16x2 d, %1, %2;\n\tmul.rn.bf16x2 %0, d, %3;\n\t}" : "=r"(r[h]) : "r"(a), "r"(b), "r"(scale2));
+    asm("{\n\t.reg .b32 d;\n\tsub.rn.bf16x2 d, %1, %2;\n\tmul.rn.bf16x2 %0, d, %3;\n\t}"
+        : "=r"(r[h])
+        : "r"(a), "r"(b), "r"(h ? scale.y : scale.x));
   }
   return make_uint2(r[0], r[1]);
 }
 
-__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
-  const uint2 r = *reinterpret_cast<const uint2*>(p);
-  return make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
-}
-__device__ __forceinline__ void st4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void st4(__nv_bfloat16* p, float4 v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+// Two 16 x 16 byte matrices, transposed: r[0], r[1] of the first, r[2], r[3] of the second.  Lane L's address
+// is row L % 16 of matrix L / 16; afterwards r[0] holds columns' bytes 4 (L % 4) .. +3 of the transposed row
+// L / 4, r[1] those of row L / 4 + 8.
+__device__ __forceinline__ void ldmatrix_t8x2(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
-// One 32 x 32 block of a warp: lane L holds row L of the accumulator in v.
+// 16 lanes x 32 columns of TMEM (16x256b, four times): in each 8 columns lane L holds columns 2 (L % 4), +1 of rows
+// L / 4 (v[0], v[1]) and L / 4 + 8 (v[2], v[3]).
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T on the CTA pair, one 256 x 256 x 16 step.
+__device__ __forceinline__ void umma_bf16_pair_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                                  uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 128 columns of the accumulator: lane = column k of out, v[j] = row n0 + j.
 template <typename TO>
-__device__ __forceinline__ void store_block(const WgradParams& p, float* stage, const float* v, int64_t row0, int64_t col0,
-                                            int lane) {
+__device__ __forceinline__ void store_columns(const WgradParams& p, const float* v, int64_t n0, int64_t k) {
+  if (k >= p.n_in) return;
   const TO* add = static_cast<const TO*>(p.add);
-  TO* out = static_cast<TO*>(p.out);
-  float4 a[8];
-  const int c = (lane & 7) * 4;
-  if (p.vec && add) {
+  TO* out = static_cast<TO*>(p.out) + n0 * p.n_in + k;
+  const int rows = (int)min((int64_t)128, p.n_out - n0);
+  if (add) {
+    add += n0 * p.n_in + k;
+    constexpr int kBatch = 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = row0 + i * 4 + (lane >> 3), col = col0 + c;
-      if (row < p.n_out && col < p.n_in) a[i] = ld4(add + row * p.n_in + col);
-    }
-  }
-  __syncwarp();
-  float4* s = reinterpret_cast<float4*>(stage + lane * kEpiPitch);
+    for (int j0 = 0; j0 < 128; j0 += kBatch) {
+      float a[kBatch];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  __syncwarp();
-  if (p.vec) {
+      for (int j = 0; j < kBatch; ++j) a[j] = j0 + j < rows ? load1(add + (int64_t)(j0 + j) * p.n_in) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + (lane >> 3);
-      const int64_t row = row0 + r, col = col0 + c;
-      if (row >= p.n_out || col >= p.n_in) continue;          // n_in % 4 == 0: the 4 columns are in range together
-      float4 d = *reinterpret_cast<const float4*>(stage + r * kEpiPitch + c);
-      if (add) {
-        d.x += a[i].x; d.y += a[i].y; d.z += a[i].z; d.w += a[i].w;
-      }
-      st4(out + row * p.n_in + col, d);
+      for (int j = 0; j < kBatch; ++j)
+        if (j0 + j < rows) store1(out + (int64_t)(j0 + j) * p.n_in, v[j0 + j] + a[j]);
     }
   } else {
-    const int64_t col = col0 + lane;
-    if (col < p.n_in) {
-#pragma unroll 4
-      for (int r = 0; r < 32; ++r) {
-        const int64_t row = row0 + r;
-        if (row >= p.n_out) break;
-        float d = stage[r * kEpiPitch + lane];
-        if (add) d += load1(add + row * p.n_in + col);
-        store1(out + row * p.n_in + col, d);
-      }
-    }
+#pragma unroll
+    for (int j = 0; j < 128; ++j)
+      if (j < rows) store1(out + (int64_t)j * p.n_in, v[j]);
   }
+}
+
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constant__ WgradParams p) {
@@ -193,21 +202,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sm.full_a[i], 1);
-      mbar_init(&sm.done_a[i], 1);
-    }
-    for (int i = 0; i < kStagesQ; ++i) {
+      mbar_init(&sm.full_b[i], 1);
+      mbar_init(&sm.done[i], 1);
       mbar_init(&sm.full_q[i], 1);
       mbar_init(&sm.empty_q[i], kGroupWarps);
-    }
-    for (int i = 0; i < kBufs; ++i) {
       mbar_init(&sm.decoded[i], 2 * kGroupWarps);
-      mbar_init(&sm.done_b[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.tfull[i], 1);
-      mbar_init(&sm.tempty[i], 2 * kEpiWarps);
-    }
+    mbar_init(sm.tfull, 1);
+    mbar_init(sm.tempty, 2 * kEpiWarps);
     mbar_init(sm.drain, 1);
     *sm.abort = 0;
     fence_barrier_init();
@@ -219,13 +221,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
   tc_fence_after();
   const uint32_t tmem = *sm.tmem;
 
-  if (warp == 0 || warp == 2) {
-    // ------------------------------------------------------------ TMA producers: dy (warp 0), q (warp 2)
-    if (lane == 0) {
+  if (warp < kFirstEpi) {
+    fewer_registers<kRegsFew>();
+    if ((warp == 0 || warp == 2) && lane == 0) {
+      // ---------------------------------------------------------- TMA producers: dy (warp 0), q (warp 2)
       const bool is_q = warp == 2;
-      const int stages = is_q ? kStagesQ : kStages;
-      uint64_t* full = is_q ? sm.full_q : sm.full_a;
-      uint64_t* freed = is_q ? sm.empty_q : sm.done_a;
+      uint64_t* full = is_q ? sm.full_q : sm.full_b;
+      uint64_t* freed = is_q ? sm.empty_q : sm.done;
       tma_prefetch_desc(is_q ? &p.q : &p.dy);
       if (is_q) tma_prefetch_desc(&p.e);
       int stage = 0;
@@ -234,29 +236,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
       for (int t = unit; ok && t < tiles; t += p.units) {
         int tm, tn;
         tile_at(p, t, tm, tn);
-        const int a0 = tm * kTile + (int)rank * 128, b0 = tn * kTile + (int)rank * 128;
-        const int e0 = (b0 / kActBlock) & ~15;
+        const int n0 = tm * kTile + (int)rank * 128, k0 = tn * kTile + (int)rank * 128;
+        const int e0 = (k0 / kActBlock) & ~15;
         for (int kb = 0; kb < p.nk; ++kb) {
           if (!mbar_poll(&freed[stage], phase ^ 1u, abort, status, kTimeoutClocks)) {
             ok = false;
             break;
           }
           if (is_q) {
-            uint8_t* at = sm.q + stage * kBytesQE;
             mbar_arrive_expect_tx(&full[stage], kBytesQE);
-            tma_load_3d(at, &p.q, &full[stage], b0, kb * kDepth, 0);
-            tma_load_3d(at + kBytesQ, &p.e, &full[stage], e0, kb * kDepth, 0);
+            tma_load_3d(sm.q + stage * kBytesQ, &p.q, &full[stage], k0, kb * kDepth, 0);
+            tma_load_3d(sm.e + stage * kBytesE, &p.e, &full[stage], e0, kb * kDepth, 0);
           } else {
             // both CTAs' halves of dy complete on the even CTA's barrier
-            uint8_t* at = sm.a + stage * kBytesA;
-            const uint32_t fa = mapa_shared(smem_u32(&full[stage]), 0);
-            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kBytesA);
-            tma_load_3d_pair(at, &p.dy, fa, a0, kb * kDepth, 0);
-            tma_load_3d_pair(at + kBytesA / 2, &p.dy, fa, a0 + 64, kb * kDepth, 0);
+            uint8_t* at = sm.b + stage * kBytesB;
+            const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kBytesB);
+            tma_load_3d_pair(at, &p.dy, fb, n0, kb * kDepth, 0);
+            tma_load_3d_pair(at + kBytesB / 2, &p.dy, fb, n0 + 64, kb * kDepth, 0);
           }
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == stages) {
+          if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -264,49 +265,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
       }
       // every issued copy must land before shared memory is given back (the odd CTA's dy is
       // counted in the even one, for which it waits at the end)
-      for (int s = 0; s < stages; ++s)
+      for (int s = 0; s < kStages; ++s)
         if ((issued & (1u << s)) && (is_q || rank == 0))
           mbar_poll(&full[s], (last_par >> s) & 1u, nullptr, status, kTimeoutClocks);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (rank == 0 && lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32_bmn(kTile, kTile) | (1u << 15);   // both operands MN-major
-      const uint64_t da0 = sdesc_mnmajor_sw128(smem_u32(sm.a), kBytesA / 2, 1024);
-      const uint64_t db0 = sdesc_mnmajor_sw128(smem_u32(sm.buf), kBytesB / 2, 1024);
-      uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0, acc = 0, acc_phase = 0;
+    } else if (warp == 1 && rank == 0 && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer (even CTA)
+      constexpr uint32_t idesc = idesc_bf16_f32_bmn(kTile, kTile);
+      const uint64_t db0 = sdesc_mnmajor_sw128(smem_u32(sm.b), kBytesB / 2, 1024);
+      uint32_t stage = 0, phase = 0, acc_phase = 0;
       bool ok = true;
       for (int t = unit; ok && t < tiles; t += p.units) {
-        if (!mbar_poll(&sm.tempty[acc], acc_phase ^ 1u, abort, status, kTimeoutClocks)) break;
+        if (!mbar_poll<true>(sm.tempty, acc_phase ^ 1u, abort, status, kTimeoutClocks)) break;
         tc_fence_after();
-        const uint32_t d = tmem + acc * (uint32_t)kTile;
         for (int kb = 0; kb < p.nk; ++kb) {
-          if (!mbar_poll(&sm.full_a[stage], phase, abort, status, kTimeoutClocks) ||
-              !mbar_poll<true>(&sm.decoded[buf], buf_phase, abort, status, kTimeoutClocks)) {
+          if (!mbar_poll(&sm.full_b[stage], phase, abort, status, kTimeoutClocks) ||
+              !mbar_poll(&sm.decoded[stage], phase, abort, status, kTimeoutClocks)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t da = da0 + stage * (uint32_t)(kBytesA / 16), db = db0 + buf * (uint32_t)(kBytesB / 16);
+          const uint64_t db = db0 + stage * (uint32_t)(kBytesB / 16);
+          const uint32_t a = tmem + kTmemA + stage * kTmemStep;
 #pragma unroll
-          for (int s = 0; s < kDepth / 16; ++s)       // 16 tokens are 2048 bytes further in either operand
-            umma_bf16_pair(d, da + s * 128, db + s * 128, idesc, (kb | s) != 0 ? 1u : 0u);
-          umma_commit_pair(&sm.done_a[stage], 0x3);
-          umma_commit_pair(&sm.done_b[buf], 0x3);
+          for (int s = 0; s < kDepth / 16; ++s)       // 16 tokens: 8 columns of TMEM, 2048 bytes of dy
+            umma_bf16_pair_ta(tmem, a + s * 8, db + s * 128, idesc, (kb | s) != 0 ? 1u : 0u);
+          umma_commit_pair(&sm.done[stage], 0x3);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
-          if (++buf == kBufs) {
-            buf = 0;
-            buf_phase ^= 1u;
-          }
         }
         if (!ok) break;
-        umma_commit_pair(&sm.tfull[acc], 0x3);
-        acc ^= 1u;
-        if (acc == 0) acc_phase ^= 1u;
+        umma_commit_pair(sm.tfull, 0x3);
+        acc_phase ^= 1u;
       }
       umma_commit_pair(sm.drain, 0x1);
       mbar_poll(sm.drain, 0, nullptr, status, kTimeoutClocks);
@@ -314,94 +305,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
     __syncwarp();
   } else if (warp < kFirstDec) {
     // ------------------------------------------------------------ epilogue
-    const int quad = warp & 3;                        // the lanes of TMEM this warp may read
-    float* stage = sm.epi + (warp - 3) * (kEpiBytes / 4);
-    uint32_t acc = 0, acc_phase = 0;
+    more_registers<kRegsEpi>();
+    const int quad = warp & 3, half = (warp - kFirstEpi) >> 2;
+    uint32_t acc_phase = 0;
     for (int t = unit; t < tiles; t += p.units) {
       int tm, tn;
       tile_at(p, t, tm, tn);
-      const int64_t row0 = (int64_t)tm * kTile + rank * 128 + quad * 32;
-      const bool w = mbar_poll(&sm.tfull[acc], acc_phase, abort, status, kTimeoutClocks);
+      const int64_t k = (int64_t)tn * kTile + rank * 128 + quad * 32 + lane;
+      const int64_t n0 = (int64_t)tm * kTile + half * 128;
+      const bool w = mbar_poll(sm.tfull, acc_phase, abort, status, kTimeoutClocks);
       if (!__all_sync(0xffffffffu, w)) break;
       tc_fence_after();
-      const uint32_t from = tmem + acc * (uint32_t)kTile + ((uint32_t)(quad * 32) << 16);
-#pragma unroll 1
-      for (int c = 0; c < kTile / 32; ++c) {
-        float v[32];
-        tmem_ld32(from + c * 32, v);
-        if (c == kTile / 32 - 1) {                    // read: the next tile's products may overwrite it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.tempty[acc]), 0));
-        }
-        const int64_t col0 = (int64_t)tn * kTile + c * 32;
-        if (row0 < p.n_out && col0 < p.n_in) {
-          if (p.out_f32) store_block<float>(p, stage, v, row0, col0, lane);
-          else store_block<__nv_bfloat16>(p, stage, v, row0, col0, lane);
-        }
+      float v[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(tmem + half * 128 + c * 32 + ((uint32_t)(quad * 32) << 16), v + 32 * c);
+      tc_fence_before();                               // read: the next tile's products may overwrite it
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(sm.tempty), 0));
+      if (n0 < p.n_out) {
+        if (p.out_f32) store_columns<float>(p, v, n0, k);
+        else store_columns<__nv_bfloat16>(p, v, n0, k);
       }
-      acc ^= 1u;
-      if (acc == 0) acc_phase ^= 1u;
+      acc_phase ^= 1u;
     }
   } else {
     // ------------------------------------------------------------ decoders
-    const int dw = warp - kFirstDec, group = dw / kGroupWarps;
-    constexpr int kIter = kDepth / 4 / kGroupWarps;   // 4 tokens a warp each time
-    const int token0 = (dw % kGroupWarps) * (4 * kIter) + (lane >> 3);
-    const int part = lane & 7;                        // 16 of the 128 columns
-    const int box = part >> 2;
-    int step = 0;                                     // of all tiles
+    fewer_registers<kRegsDec>();
+    const int dw = warp - kFirstDec, group = dw / kGroupWarps, quad = warp & 3;   // 32 columns: one block
+    uint16_t* scales = sm.scales + dw * kDepth;
+    // ldmatrix row of this lane: token lane % 16 of a group of 16, columns 16 (lane / 16) .. +15 of the block
+    const int chunk = quad * 2 + (lane >> 4);
+    const uint32_t row_at = (uint32_t)((lane & 15) * 128 + ((chunk ^ (lane & 7)) << 4));
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    int step = 0;                                      // of all tiles
     bool ok = true;
     for (int t = unit; ok && t < tiles; t += p.units) {
       int tm, tn;
       tile_at(p, t, tm, tn);
-      const int e_at = (((tn * kTile + (int)rank * 128) / kActBlock) & 15) + (part >> 1);
+      const int e_at = (((tn * kTile + (int)rank * 128) / kActBlock) & 15) + quad;
       for (int kb = 0; kb < p.nk; ++kb, ++step) {
         if (step % kDecGroups != group) continue;
-        const int stage = step % kStagesQ;
-        bool w = mbar_poll(&sm.full_q[stage], (uint32_t)(step / kStagesQ) & 1u, abort, status, kTimeoutClocks);
+        const int stage = step % kStages;
+        const uint32_t phase = (uint32_t)(step / kStages) & 1u;
+        bool w = mbar_poll(&sm.full_q[stage], phase, abort, status, kTimeoutClocks);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
         }
-        const uint8_t* q = sm.q + stage * kBytesQE;
-        const uint8_t* e = q + kBytesQ;
-        uint4 raw[kIter];
-        uint32_t sb[kIter];
+        const uint8_t* e = sm.e + stage * kBytesE;
+        const uint32_t q = smem_u32(sm.q + stage * kBytesQ) + row_at;
+        uint32_t raw[4][4];
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-          raw[i] = *reinterpret_cast<const uint4*>(q + (token0 + 4 * i) * 128 + part * 16);
-          sb[i] = e[(token0 + 4 * i) * 16 + e_at];
+        for (int g = 0; g < 4; ++g) ldmatrix_t8x2(q + g * (16 * 128), raw[g]);
+        // the step's 64 scales as bf16, two a lane, for the whole warp
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t b = e[(lane + 32 * h) * 16 + e_at];
+          scales[lane + 32 * h] = (uint16_t)(b == 255u ? 0x7FC0u : b << 7);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty_q[stage]);
-        // the products that read the buffer last are done
-        const int buf = step % kBufs;
-        w = mbar_poll(&sm.done_b[buf], ((uint32_t)(step / kBufs) & 1u) ^ 1u, abort, status, kTimeoutClocks);
-        if (!__all_sync(0xffffffffu, w)) {
+        uint2 s[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) s[g] = *reinterpret_cast<const uint2*>(scales + 16 * g + 4 * (lane & 3));
+        // the products that read this part of TMEM last are done
+        w = mbar_poll(&sm.done[stage], phase ^ 1u, abort, status, kTimeoutClocks);
+        if (!__all_sync(0xffffffffu, w)) {             // (also: every lane has its scales)
           ok = false;
           break;
         }
-        uint8_t* b = sm.buf + buf * kBytesB + box * (kBytesB / 2);
+        tc_fence_after();
+        const uint32_t to = tmem + kTmemA + stage * kTmemStep + lanes;
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-          const int token = token0 + 4 * i;
-          const uint32_t s1 = sb[i] == 255u ? 0x7FC0u : sb[i] << 7;    // 2^E in bf16
-          const uint32_t s2 = s1 | (s1 << 16);
-          const uint2 d0 = decode4(raw[i].x, s2), d1 = decode4(raw[i].y, s2), d2 = decode4(raw[i].z, s2),
-                      d3 = decode4(raw[i].w, s2);
-          // the two 16-byte chunks, swizzled by the token; lanes of the second box write their second
-          // chunk first, so that 8 lanes cover all banks
-          const int c0 = (part & 3) * 2;
-          const uint4 lo = make_uint4(d0.x, d0.y, d1.x, d1.y), hi = make_uint4(d2.x, d2.y, d3.x, d3.y);
-          uint8_t* row = b + token * 128;
-          const int sw = token & 7;
-          *reinterpret_cast<uint4*>(row + (((c0 + box) ^ sw) << 4)) = box ? hi : lo;
-          *reinterpret_cast<uint4*>(row + (((c0 + 1 - box) ^ sw) << 4)) = box ? lo : hi;
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[16];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint2 lo = decode4(raw[g][2 * h], s[g]), hi = decode4(raw[g][2 * h + 1], s[g]);
+            v[4 * g] = lo.x;
+            v[4 * g + 1] = lo.y;
+            v[4 * g + 2] = hi.x;
+            v[4 * g + 3] = hi.y;
+          }
+          tmem_st_16x32(to + ((uint32_t)(16 * h) << 16), v);
         }
-        fence_proxy_async_smem();
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&sm.decoded[buf]), 0));
+        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&sm.decoded[stage]), 0));
       }
     }
   }
@@ -529,7 +520,7 @@ extern "C" int cz_act_wgrad(const void* dy, int64_t ld_dy, const void* ckpt, int
   const uint8_t* ck = static_cast<const uint8_t*>(ckpt);
   WgradParams p;
   if (!encode_map(&p.dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, n_out, rows, ld_dy * 2, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, ck, l.ld_q, rows, l.ld_q, 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_map(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, ck, l.ld_q, rows, l.ld_q, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_map(&p.e, CU_TENSOR_MAP_DATA_TYPE_UINT8, ck + l.e_off, l.ld_e, rows, l.ld_e, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
     return CZ_ERR_CUDA;
   p.add = add;
@@ -542,9 +533,6 @@ extern "C" int cz_act_wgrad(const void* dy, int64_t ld_dy, const void* ckpt, int
   p.tiles_n = (int32_t)tiles_n;
   p.units = (int32_t)std::min<int64_t>(units, tiles_m * tiles_n);
   p.out_f32 = out_dtype == CZ_F32;
-  // 4 elements at a time: 16 bytes of fp32, 8 of bf16
-  const uintptr_t b = (uintptr_t)dtype_bytes(out_dtype) * 4;
-  p.vec = n_in % 4 == 0 && aligned(out, b) && aligned(add, b);
   // the cluster dimension is the kernel's own
   return launch_kernel(wgrad_kernel, dim3((unsigned)(2 * p.units)), dim3(kThreads), kSmemBytes, s, 1, p);
 }
