@@ -9,13 +9,14 @@
 // that is 81 KB a step and SM, 633 clocks at 128 bytes a clock against the 512 of the products (measured:
 // 1.69 ms for 8192 x 25600 x 5120); this way it is 49 KB.  dy is the B operand, MN-major (the sum runs over
 // its rows).  TMEM: 256 columns of accumulator, 8 x 32 of decoded steps.  Lanes of the accumulator run along k, so
-// the epilogue reads add and writes out 128 bytes a warp without staging; it takes the whole
-// accumulator into registers first, and the next tile's products start.  Per CTA:
+// the epilogue reads add and writes out 128 bytes a warp without staging; it takes its second half of
+// the accumulator into registers before it stores it, and the next tile's products start.  Per CTA:
 //   warp 0       TMA producer of dy (128-byte swizzle)
 //   warp 1       TMEM allocation and, in the even CTA, the thread that issues tcgen05.mma
-//   warp 2       TMA producer of q and its scale bytes, which runs ahead by itself
+//   warp 2       TMA producer of q, which runs ahead by itself
 //   warps 4-11   epilogue, two a quarter of the lanes
-//   warps 12-19  decoders: two groups of four warps take steps in turn
+//   warp 3       the scale bytes of q, 4 a token (cp.async: as a tensor copy 64 rows of 16 bytes a step cost 8%)
+//   warps 12-23  decoders: three groups of four warps take steps in turn
 // A decoder transposes 16 x 16 bytes with ldmatrix, which leaves 4 tokens of one column in a
 // register, and a byte q becomes bf16 without integer conversion: 0x4300 | (q & 127) is 128 + (q & 127),
 // 0x4300 | (q & 128) is 128 or 256, and their difference is q (exact); one more multiplication
@@ -37,17 +38,17 @@ namespace {
 constexpr int kTile = 256;                 // rows and columns of a pair's tile
 constexpr int kDepth = 64;                 // tokens a step
 constexpr int kStages = 8;                 // steps in flight: dy and q in shared memory, decoded in TMEM
-constexpr int kBytesB = 128 * kDepth * 2, kBytesQ = 128 * kDepth, kBytesE = 16 * kDepth;
-constexpr int kBytesQE = kBytesQ + kBytesE;
-constexpr int kEpiWarps = 8, kDecWarps = 8;
-constexpr int kDecGroups = 2, kGroupWarps = kDecWarps / kDecGroups;   // the groups take steps in turn
+constexpr int kBytesB = 128 * kDepth * 2, kBytesQ = 128 * kDepth, kBytesE = 4 * kDepth;
+constexpr int kEpiWarps = 8;
+constexpr int kDecGroups = 3, kGroupWarps = 4, kDecWarps = kDecGroups * kGroupWarps;   // the groups take steps in turn
 constexpr int kFirstEpi = 4, kFirstDec = kFirstEpi + kEpiWarps;
 constexpr int kThreads = 32 * (kFirstDec + kDecWarps);
-// Registers: 96 a thread at launch, 640 x 96 = 61440; then 128 x 48 + 256 x 152 + 256 x 64 = 61440.
-constexpr int kRegsFew = 48, kRegsEpi = 152, kRegsDec = 64;
-static_assert(128 * kRegsFew + 32 * kEpiWarps * kRegsEpi + 32 * kDecWarps * kRegsDec <= kThreads * 96, "register split");
+// Registers: at launch what 65536 allow every thread, then shared out anew.
+constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
+constexpr int kRegsFew = 48, kRegsEpi = 112, kRegsDec = 64;
+static_assert(128 * kRegsFew + 32 * kEpiWarps * kRegsEpi + 32 * kDecWarps * kRegsDec <= kThreads * kRegsLaunch, "register split");
 constexpr int kScaleBytes = 2 * kDepth;    // a decoder warp's scales of a step, bf16
-constexpr int kSmemBytes = 1024 + kStages * (kBytesB + kBytesQE) + kDecWarps * kScaleBytes + 512;
+constexpr int kSmemBytes = 1024 + kStages * (kBytesB + kBytesQ + kBytesE) + kDecWarps * kScaleBytes + 512;
 constexpr uint32_t kTmemCols = 512, kTmemA = 256, kTmemStep = kDepth / 2;
 constexpr int64_t kTimeoutClocks = 4000000000LL;   // about 2 s
 static_assert(kBytesB % 1024 == 0 && kBytesQ % 1024 == 0, "swizzle atoms");
@@ -55,7 +56,9 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 static_assert(kTmemA + kStages * kTmemStep <= kTmemCols, "tensor memory");
 
 struct WgradParams {
-  CUtensorMap dy, q, e;
+  CUtensorMap dy, q;
+  const uint8_t* e;          // scale bytes, rows ld_e apart
+  int64_t rows, ld_e;
   const void* add;
   void* out;
   int32_t* status;
@@ -155,18 +158,18 @@ __device__ __forceinline__ void umma_bf16_pair_ta(uint32_t tmem_d, uint32_t tmem
       : "memory");
 }
 
-// 128 columns of the accumulator: lane = column k of out, v[j] = row n0 + j.
+// 64 columns of the accumulator: lane = column k of out, v[j] = row n0 + j.
 template <typename TO>
 __device__ __forceinline__ void store_columns(const WgradParams& p, const float* v, int64_t n0, int64_t k) {
   if (k >= p.n_in) return;
   const TO* add = static_cast<const TO*>(p.add);
   TO* out = static_cast<TO*>(p.out) + n0 * p.n_in + k;
-  const int rows = (int)min((int64_t)128, p.n_out - n0);
+  const int rows = (int)min((int64_t)64, p.n_out - n0);
   if (add) {
     add += n0 * p.n_in + k;
-    constexpr int kBatch = 8;
+    constexpr int kBatch = 16;
 #pragma unroll
-    for (int j0 = 0; j0 < 128; j0 += kBatch) {
+    for (int j0 = 0; j0 < 64; j0 += kBatch) {
       float a[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) a[j] = j0 + j < rows ? load1(add + (int64_t)(j0 + j) * p.n_in) : 0.f;
@@ -176,7 +179,7 @@ __device__ __forceinline__ void store_columns(const WgradParams& p, const float*
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 128; ++j)
+    for (int j = 0; j < 64; ++j)
       if (j < rows) store1(out + (int64_t)j * p.n_in, v[j]);
   }
 }
@@ -204,7 +207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.full_b[i], 1);
       mbar_init(&sm.done[i], 1);
-      mbar_init(&sm.full_q[i], 1);
+      mbar_init(&sm.full_q[i], 1 + 32);
       mbar_init(&sm.empty_q[i], kGroupWarps);
       mbar_init(&sm.decoded[i], 2 * kGroupWarps);
     }
@@ -229,7 +232,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
       uint64_t* full = is_q ? sm.full_q : sm.full_b;
       uint64_t* freed = is_q ? sm.empty_q : sm.done;
       tma_prefetch_desc(is_q ? &p.q : &p.dy);
-      if (is_q) tma_prefetch_desc(&p.e);
       int stage = 0;
       uint32_t phase = 0, issued = 0, last_par = 0;
       bool ok = true;
@@ -237,16 +239,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
         int tm, tn;
         tile_at(p, t, tm, tn);
         const int n0 = tm * kTile + (int)rank * 128, k0 = tn * kTile + (int)rank * 128;
-        const int e0 = (k0 / kActBlock) & ~15;
         for (int kb = 0; kb < p.nk; ++kb) {
           if (!mbar_poll(&freed[stage], phase ^ 1u, abort, status, kTimeoutClocks)) {
             ok = false;
             break;
           }
           if (is_q) {
-            mbar_arrive_expect_tx(&full[stage], kBytesQE);
+            mbar_arrive_expect_tx(&full[stage], kBytesQ);
             tma_load_3d(sm.q + stage * kBytesQ, &p.q, &full[stage], k0, kb * kDepth, 0);
-            tma_load_3d(sm.e + stage * kBytesE, &p.e, &full[stage], e0, kb * kDepth, 0);
           } else {
             // both CTAs' halves of dy complete on the even CTA's barrier
             uint8_t* at = sm.b + stage * kBytesB;
@@ -275,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
       uint32_t stage = 0, phase = 0, acc_phase = 0;
       bool ok = true;
       for (int t = unit; ok && t < tiles; t += p.units) {
-        if (!mbar_poll<true>(sm.tempty, acc_phase ^ 1u, abort, status, kTimeoutClocks)) break;
+        if (!mbar_poll(sm.tempty, acc_phase ^ 1u, abort, status, kTimeoutClocks)) break;
         tc_fence_after();
         for (int kb = 0; kb < p.nk; ++kb) {
           if (!mbar_poll(&sm.full_b[stage], phase, abort, status, kTimeoutClocks) ||
@@ -302,6 +302,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
       umma_commit_pair(sm.drain, 0x1);
       mbar_poll(sm.drain, 0, nullptr, status, kTimeoutClocks);
     }
+    if (warp == 3) {
+      // ---------------------------------------------------------- the scale bytes of q, 4 a token
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = unit; ok && t < tiles; t += p.units) {
+        int tm, tn;
+        tile_at(p, t, tm, tn);
+        const int64_t col = (tn * kTile + (int)rank * 128) / kActBlock;
+        const bool in = col < p.ld_e;                   // both are multiples of 4
+        for (int kb = 0; kb < p.nk; ++kb) {
+          const bool w = mbar_poll(&sm.empty_q[stage], phase ^ 1u, abort, status, kTimeoutClocks);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t token = (int64_t)kb * kDepth + lane + 32 * h;
+            const bool live = in && token < p.rows;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(sm.e + stage * kBytesE + (lane + 32 * h) * 4)),
+                         "l"(live ? p.e + token * p.ld_e + col : p.e), "r"(live ? 4 : 0)
+                         : "memory");
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.full_q[stage])) : "memory");
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
     __syncwarp();
   } else if (warp < kFirstDec) {
     // ------------------------------------------------------------ epilogue
@@ -316,15 +349,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
       const bool w = mbar_poll(sm.tfull, acc_phase, abort, status, kTimeoutClocks);
       if (!__all_sync(0xffffffffu, w)) break;
       tc_fence_after();
-      float v[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tmem + half * 128 + c * 32 + ((uint32_t)(quad * 32) << 16), v + 32 * c);
-      tc_fence_before();                               // read: the next tile's products may overwrite it
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(sm.tempty), 0));
-      if (n0 < p.n_out) {
-        if (p.out_f32) store_columns<float>(p, v, n0, k);
-        else store_columns<__nv_bfloat16>(p, v, n0, k);
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        float v[64];
+        const uint32_t from = tmem + half * 128 + c * 64 + ((uint32_t)(quad * 32) << 16);
+        tmem_ld32(from, v);
+        tmem_ld32(from + 32, v + 32);
+        if (c == 1) {                                  // read: the next tile's products may overwrite it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(sm.tempty), 0));
+        }
+        if (n0 + c * 64 < p.n_out) {
+          if (p.out_f32) store_columns<float>(p, v, n0 + c * 64, k);
+          else store_columns<__nv_bfloat16>(p, v, n0 + c * 64, k);
+        }
       }
       acc_phase ^= 1u;
     }
@@ -340,9 +379,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
     int step = 0;                                      // of all tiles
     bool ok = true;
     for (int t = unit; ok && t < tiles; t += p.units) {
-      int tm, tn;
-      tile_at(p, t, tm, tn);
-      const int e_at = (((tn * kTile + (int)rank * 128) / kActBlock) & 15) + quad;
       for (int kb = 0; kb < p.nk; ++kb, ++step) {
         if (step % kDecGroups != group) continue;
         const int stage = step % kStages;
@@ -360,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
         // the step's 64 scales as bf16, two a lane, for the whole warp
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t b = e[(lane + 32 * h) * 16 + e_at];
+          const uint32_t b = e[(lane + 32 * h) * 4 + quad];
           scales[lane + 32 * h] = (uint16_t)(b == 255u ? 0x7FC0u : b << 7);
         }
         __syncwarp();
@@ -520,9 +556,11 @@ extern "C" int cz_act_wgrad(const void* dy, int64_t ld_dy, const void* ckpt, int
   const uint8_t* ck = static_cast<const uint8_t*>(ckpt);
   WgradParams p;
   if (!encode_map(&p.dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, n_out, rows, ld_dy * 2, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, ck, l.ld_q, rows, l.ld_q, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map(&p.e, CU_TENSOR_MAP_DATA_TYPE_UINT8, ck + l.e_off, l.ld_e, rows, l.ld_e, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
+      !encode_map(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, ck, l.ld_q, rows, l.ld_q, 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return CZ_ERR_CUDA;
+  p.e = ck + l.e_off;
+  p.rows = rows;
+  p.ld_e = l.ld_e;
   p.add = add;
   p.out = out;
   p.status = static_cast<int32_t*>(workspace);

@@ -105,36 +105,40 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// As mbar_try_wait / mbar_wait, acquiring at cluster scope: for barriers on which the peer
-// CTA's threads arrive to hand over data in its shared memory.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// As mbar_wait, for waits that block in every step of a chain: the bound is read from the SM's
-// own clock, and only after some polls (%globaltimer costs most of a microsecond).
+// As mbar_wait, for warps that share their SM with arithmetic: the hardware holds the thread for up to
+// kHoldNs a try, so a long wait takes no issue slots, and the bound is read from the SM's own clock.
+// CLUSTER: acquires at cluster scope.
+constexpr uint32_t kHoldNs = 1000000;
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
                                           int64_t clocks) {
   int64_t t0 = 0;
   for (uint32_t it = 0;; ++it) {
-    if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    if ((it & 255u) == 255u) {
-      if (abort && *abort) return false;
-      const int64_t now = clock64();
-      if (it == 255u) t0 = now;
-      else if (now - t0 > clocks) {
-        record_status(status, CZ_ERR_TIMEOUT);
-        if (abort) *abort = 1;
-        return false;
-      }
+    uint32_t ok;
+    if constexpr (CLUSTER)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(kHoldNs)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(kHoldNs)
+          : "memory");
+    if (ok) return true;
+    if (abort && *abort) return false;
+    const int64_t now = clock64();
+    if (it == 0) t0 = now;
+    else if (now - t0 > clocks) {
+      record_status(status, CZ_ERR_TIMEOUT);
+      if (abort) *abort = 1;
+      return false;
     }
   }
 }
