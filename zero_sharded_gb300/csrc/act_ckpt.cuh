@@ -19,6 +19,10 @@
 
 #include <stdint.h>
 
+#ifdef __CUDACC__
+#include "vec8.cuh"
+#endif
+
 namespace cz {
 
 constexpr int kActBlock = 32;
@@ -97,11 +101,27 @@ __device__ __forceinline__ uint32_t act_encode1(float v, uint32_t* q) {
   return b;
 }
 
+// q + 128 as the low mantissa byte of 2^23: one difference gives q, one product x^ (both exact; integer
+// conversions run at an eighth of the rate).
 __device__ __forceinline__ void act_decode8(uint2 q, uint32_t b, float* v) {
   const float s = act_scale(b);
-  const uint32_t w[2] = {q.x, q.y};
+  const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)(w[j >> 2] >> (8 * (j & 3))) * s;
+  for (int j = 0; j < 8; ++j)
+    v[j] = (__uint_as_float(__byte_perm(w[j >> 2], 0x4B000000u, 0x7540u | (uint32_t)(j & 3))) - 8388736.f) * s;
+}
+
+// The 8 values of w (q), scaled by s: s = 2^E, or 2^E times a factor to round once.
+__device__ __forceinline__ F8 act_values8(uint2 q, float s) {
+  const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
+  F8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = __byte_perm(w[i >> 1], 0x4B000000u, 0x7540u | (uint32_t)(2 * (i & 1)));
+    const uint32_t b = __byte_perm(w[i >> 1], 0x4B000000u, 0x7540u | (uint32_t)(2 * (i & 1) + 1));
+    v.p[i] = mul2(add2(make_float2(__uint_as_float(a), __uint_as_float(b)), both(-8388736.f)), both(s));
+  }
+  return v;
 }
 
 __device__ __forceinline__ float act_decode1(uint8_t q, uint32_t b) { return (float)(int8_t)q * act_scale(b); }

@@ -53,13 +53,14 @@ bool opt_matrix_ok(const void* p, const cz_norm_args& a, int64_t ld, int64_t byt
   return p == nullptr || matrix_ok(p, a.rows, a.cols, ld, bytes);
 }
 
-NormParams params_of(const cz_norm_args& a) {
+// `wide`: 8 elements a thread up to 1024 threads a row.
+NormParams params_of(const cz_norm_args& a, bool wide) {
   NormParams p{};
   p.rows = a.rows;
   p.cols = (int32_t)a.cols;
-  // 8 elements a thread while a row fits 512 threads, then 16: a row of the backward holds
-  // six fp32 values an element in registers
-  const int64_t per = a.cols <= 8 * 512 ? 8 : 16;
+  // The backward holds eight fp32 values an element in registers: 8 elements a thread as long as a row
+  // fits 1024 threads.  The forward holds four: 16 a thread from 512 threads on.
+  const int64_t per = a.cols <= 8 * (wide ? 1024 : 512) ? 8 : 16;
   p.row_threads = (int32_t)round_up(div_up(a.cols, per), 32);
   p.rows_per_block = std::max(1, 256 / p.row_threads);   // narrow rows share a block of up to 8 warps
   p.post = a.post_norm;
@@ -123,7 +124,7 @@ extern "C" int cz_block_norm_fwd(const cz_norm_args* args, void* stream) {
   const int dev = check_sm103();
   if (dev != CZ_OK) return dev;
   NvtxRange range("cz/block_norm_fwd");
-  NormParams p = params_of(a);
+  NormParams p = params_of(a, false);
   p.h_out = a.h_out;
   p.x = a.x;
   p.ld_h_out = a.ld_h_out;
@@ -177,7 +178,7 @@ extern "C" int cz_block_norm_bwd(const cz_norm_args* args, void* stream) {
   const int dev = check_sm103();
   if (dev != CZ_OK) return dev;
   NvtxRange range("cz/block_norm_bwd");
-  NormParams p = params_of(a);
+  NormParams p = params_of(a, true);
   p.dx = a.dx;
   p.dh_in = a.dh_in;
   p.dh = a.dh;
@@ -194,7 +195,7 @@ extern "C" int cz_block_norm_bwd(const cz_norm_args* args, void* stream) {
                    rows_aligned(a.dh_in, a.ld_dh_in, hb) && rows_aligned(a.dh, a.ld_dh, hb) &&
                    rows_aligned(a.dy, a.ld_dy, yb) &&
                    (!token || (rows_aligned(a.gate, a.ld_gate, yb) && rows_aligned(a.dgate, a.ld_dgate, yb)));
-  const int blocks = (int)std::min<int64_t>(div_up(a.rows, p.rows_per_block), std::min(kMaxBlocks, 2 * sm_count()));
+  const int blocks = (int)std::min<int64_t>(div_up(a.rows, p.rows_per_block), std::min(kMaxBlocks, norm_bwd_blocks_per_sm(p) * sm_count()));
   if (blocks > 0) {
     const int r = launch_norm_bwd(p, a.h_dtype == CZ_F32, a.y_dtype == CZ_F32, vec, blocks, stream);
     if (r != CZ_OK) return r;

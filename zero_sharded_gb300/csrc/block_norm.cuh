@@ -153,25 +153,6 @@ __device__ __forceinline__ void keep_chunk(uint8_t* ck, const ActLayout& l, int6
   }
 }
 
-// The chunk's values of a kept row.
-template <bool VEC>
-__device__ __forceinline__ void kept_chunk(const uint8_t* ck, const ActLayout& l, int64_t row, float* v, int c, int t, int n) {
-  if constexpr (VEC) {
-    const int col = col_of<true>(c, 0, t, n);
-    if (col < l.ld_q) {
-      act_decode8(__ldcs(reinterpret_cast<const uint2*>(ck + row * l.ld_q + col)),
-                  ck[l.e_off + row * l.ld_e + col / kActBlock], v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<false>(c, j, t, n);
-      v[j] = col < l.ld_q ? act_decode1(ck[row * l.ld_q + col], ck[l.e_off + row * l.ld_e + col / kActBlock]) : 0.f;
-    }
-  }
-}
+__device__ __forceinline__ int round4(int v) { return (v + 3) & ~3; }
 
 }  // namespace cz

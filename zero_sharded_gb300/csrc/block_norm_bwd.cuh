@@ -1,0 +1,510 @@
+// Backward of the norms around a block (forward: block_norm_fwd.cu).  With the stored
+// r_h, r_y, h^ = h' r_h and y^ = y r_y:
+//   c  = mean_j(w_pre dx h^);      D  = dh' + r_h (w_pre dx - h^ c);   dw_pre  = sum_t dx h^
+//   dh = h_scale D;                dn = y_scale act(gate) D;           dw_post = sum_t dn y^
+//   dgate = y_scale act'(gate) n D, n = y^ w_post  (summed over t for a channel gate)
+//   e  = mean_j(w_post dn y^);     dy = r_y (w_post dn - y^ e)         (dy = dn without the post-norm)
+//
+// Bound by memory: dx, dh', h', y in, dh, dy out; h' and y at 33/32 bytes from a
+// checkpoint.  A group of threads walks over rows; asynchronous copies bring the rows ahead into a
+// ring in shared memory, where the vectors over the columns (weights, gate) lie too, so that registers
+// hold the column sums of the weight gradients and one row only.  The two sums over
+// a row's columns cost one barrier a row: the second sum of row i and the first of row i + 1 are joined together,
+// and dy of row i is written after it.  The arithmetic runs on pairs (two fp32 an instruction): one
+// SM has 2300 clocks for a row of 5120 columns at the memory's rate, and as many instructions as that allows.  The
+// groups' column sums are added in a fixed order by a second kernel, so results do not depend on timing.
+//
+// This file is compiled once for each type of the residual stream.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "block_norm.cuh"
+#include "train_ops.h"
+
+namespace cz {
+namespace {
+
+// A row's inputs in shared memory: byte offsets within a stage.
+struct Stage {
+  int32_t dx, dh, h, h_e, y, y_e, gate, bytes;
+};
+
+struct BwdLayout {
+  Stage at;
+  int32_t stages;            // 0: rows are read from memory where they are used
+  int32_t vectors;           // floats of the vectors over the columns, which come first
+  int32_t v_pre, v_post;     // w_pre, w_post; < 0: not there
+  int32_t v_gate, v_slope;   // channel gate: y_scale act(gate), y_scale act'(gate) w_post
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// `bytes` bytes (a multiple of 16, 16-byte aligned) by the n threads of a row.
+__device__ __forceinline__ void copy_bytes16(uint32_t dst, const uint8_t* src, int bytes, int t, int n) {
+  for (int i = t * 16; i < bytes; i += n * 16) cp_async16(dst + i, src + i);
+}
+
+// One row of a rows x cols matrix.  Rows at any alignment are copied in 4-byte words: a bf16 row that starts in the
+// middle of a word takes its neighbour's half word along, except past either end of the matrix.
+template <typename T, bool VEC>
+__device__ __forceinline__ void copy_row(uint8_t* dst, const void* base, int64_t row, int64_t rows, int64_t ld, int cols, int t,
+                                         int n) {
+  const T* src = static_cast<const T*>(base) + row * ld;
+  const uint32_t to = smem_u32(dst);
+  if constexpr (VEC) {
+    copy_bytes16(to, reinterpret_cast<const uint8_t*>(src), cols * (int)sizeof(T), t, n);
+  } else if constexpr (sizeof(T) == 4) {
+    for (int i = t; i < cols; i += n) cp_async4(to + 4 * i, src + i, 4);
+  } else {
+    const int off = (int)(reinterpret_cast<uintptr_t>(src) & 2);
+    const uint8_t* word = reinterpret_cast<const uint8_t*>(src) - off;
+    const int words = (off + 2 * cols + 3) / 4;
+    for (int i = t; i < words; i += n) {
+      if (i == 0 && off && row == 0)        // nothing before the matrix is read
+        *reinterpret_cast<T*>(dst + 2) = *src;
+      else
+        cp_async4(to + 4 * i, word + 4 * i, (row == rows - 1 && 4 * i + 2 == off + 2 * cols) ? 2 : 4);
+    }
+  }
+}
+
+// The chunk's values of a row in shared memory (RING) or in memory.
+template <typename T, bool VEC, bool RING>
+__device__ __forceinline__ F8 take(const uint8_t* stage, const void* base, int64_t row, int64_t ld, int c, int t, int n, int cols) {
+  F8 v;
+  if constexpr (VEC) {
+    const int col = col_of<true>(c, 0, t, n);
+    Raw8<T> r;
+    zero8(r);
+    if (col < cols) {
+      if constexpr (RING) {
+        const uint4* s = reinterpret_cast<const uint4*>(stage + col * (int)sizeof(T));
+        r.a = s[0];
+        if constexpr (sizeof(T) == 4) r.b = s[1];
+      } else {
+        load8(static_cast<const T*>(base) + row * ld + col, r);
+      }
+    }
+    v = values(r);
+  } else {
+    const T* src = static_cast<const T*>(base) + row * ld;
+    const T* s = RING ? reinterpret_cast<const T*>(stage + (sizeof(T) == 2 ? (reinterpret_cast<uintptr_t>(src) & 2) : 0)) : src;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = col_of<false>(c, j, t, n);
+      v.set(j, col < cols ? load1(s + col) : 0.f);
+    }
+  }
+  return v;
+}
+
+// The chunk's values of a kept row times `factor`, each rounded once.
+template <bool VEC, bool RING>
+__device__ __forceinline__ F8 take_kept(const uint8_t* q, const uint8_t* e, const uint8_t* ck, const ActLayout& l, int64_t row,
+                                        float factor, int c, int t, int n) {
+  F8 v;
+  if constexpr (!RING) {
+    q = ck + row * l.ld_q;
+    e = ck + l.e_off + row * l.ld_e;
+  }
+  if constexpr (VEC) {
+    const int col = col_of<true>(c, 0, t, n);
+    if (col < l.ld_q) v = act_values8(*reinterpret_cast<const uint2*>(q + col), act_scale(e[col / kActBlock]) * factor);
+    else v.fill(0.f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = col_of<false>(c, j, t, n);
+      v.set(j, col < l.ld_q ? act_decode1(q[col], e[col / kActBlock]) * factor : 0.f);
+    }
+  }
+  return v;
+}
+
+// 8 elements of a vector over the columns, in shared memory (RING) or memory.
+template <bool VEC, bool RING>
+__device__ __forceinline__ F8 take_vector(const float* w, int c, int t, int n, int cols) {
+  F8 v;
+  if constexpr (VEC) {
+    const int col = col_of<true>(c, 0, t, n);
+    v.fill(0.f);
+    if (col < cols) {
+      if (RING || (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+        const float4 a = *reinterpret_cast<const float4*>(w + col), b = *reinterpret_cast<const float4*>(w + col + 4);
+        v.p[0] = make_float2(a.x, a.y);
+        v.p[1] = make_float2(a.z, a.w);
+        v.p[2] = make_float2(b.x, b.y);
+        v.p[3] = make_float2(b.z, b.w);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v.set(j, w[col + j]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = col_of<false>(c, j, t, n);
+      v.set(j, col < cols ? w[col] : 0.f);
+    }
+  }
+  return v;
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void put(T* row, const F8& v, int c, int t, int n, int cols) {
+  if constexpr (VEC) {
+    const int col = col_of<true>(c, 0, t, n);
+    if (col < cols) store8(row + col, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = col_of<false>(c, j, t, n);
+      if (col < cols) store1(row + col, v.get(j));
+    }
+  }
+}
+
+// Barrier of the n threads of row group g.
+template <bool SOLO>
+__device__ __forceinline__ void group_sync(int g, int n) {
+  if constexpr (SOLO) __syncthreads();
+  else if (n == 32) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(n) : "memory");
+}
+
+// Sums of a and b over the threads of a row group; `red` alternates between two arrays.
+template <bool SOLO>
+__device__ __forceinline__ float2 group_sum(float2 a, float2* red, int g, int n, int row_warps) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+    a = add2(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, d), __shfl_xor_sync(0xffffffffu, a.y, d)));
+  if (row_warps == 1) {
+    group_sync<SOLO>(g, n);
+    return a;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[warp] = a;
+  group_sync<SOLO>(g, n);
+  a = lane < row_warps ? red[g * row_warps + lane] : make_float2(0.f, 0.f);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+    a = add2(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, d), __shfl_xor_sync(0xffffffffu, a.y, d)));
+  return a;
+}
+
+__device__ __forceinline__ float sum8(const F8& v) {
+  const float2 s = add2(add2(v.p[0], v.p[1]), add2(v.p[2], v.p[3]));
+  return s.x + s.y;
+}
+
+// SOLO: one row group a block.  CHANNEL: a channel gate.
+template <typename TH, typename TY, bool VEC, int C, int MAXT, bool SOLO, bool RING, bool CHANNEL>
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(const __grid_constant__ NormParams p,
+                                                                           const __grid_constant__ BwdLayout lay) {
+  __shared__ float2 red[2][32];
+  extern __shared__ __align__(16) uint8_t dyn[];
+  const int n = SOLO ? (int)blockDim.x : p.row_threads;
+  const int g = SOLO ? 0 : threadIdx.x / n, t = threadIdx.x - g * n, row_warps = n >> 5;
+  const float inv_n = 1.f / (float)p.cols;
+  const bool token = !CHANNEL && p.gate_kind == kGateToken, weighted = p.post && p.w_post;
+  const int cols = p.cols;
+  float* vec = reinterpret_cast<float*>(dyn);
+  uint8_t* ring = dyn + lay.vectors * 4 + g * (lay.stages * lay.at.bytes);
+  if constexpr (RING) {
+    for (int i = threadIdx.x; i < cols; i += blockDim.x) {
+      if (lay.v_pre >= 0) vec[lay.v_pre + i] = p.w_pre[i];
+      if (lay.v_post >= 0) vec[lay.v_post + i] = p.w_post[i];
+      if constexpr (CHANNEL) {
+        float value, slope;
+        gate_value_slope(static_cast<const float*>(p.gate)[i], p.gate_act, value, slope);
+        vec[lay.v_gate + i] = p.y_scale * value;
+        vec[lay.v_slope + i] = p.y_scale * slope * (weighted ? p.w_post[i] : 1.f);
+      }
+    }
+    __syncthreads();
+  }
+  const int groups = SOLO ? 1 : p.rows_per_block;
+  const int64_t stride = (int64_t)gridDim.x * groups;
+  const int64_t row0 = (int64_t)blockIdx.x * groups + g;
+  const int count = row0 < p.rows ? (int)((p.rows - row0 + stride - 1) / stride) : 0;   // rows of this group
+
+  auto issue = [&](int i, int stage) {       // the copies of the group's i-th row
+    if constexpr (RING) {
+      if (i < count) {
+        const int64_t row = row0 + i * stride;
+        uint8_t* st = ring + stage * lay.at.bytes;
+        if (p.pre) copy_row<TY, VEC>(st + lay.at.dx, p.dx, row, p.rows, p.ld_dx, cols, t, n);
+        if (p.dh_in) copy_row<TH, VEC>(st + lay.at.dh, p.dh_in, row, p.rows, p.ld_dh_in, cols, t, n);
+        if (p.pre) {
+          if (p.h_ckpt) {
+            copy_bytes16(smem_u32(st + lay.at.h), p.h_ckpt + row * p.ck.ld_q, (int)p.ck.ld_q, t, n);
+            copy_bytes16(smem_u32(st + lay.at.h_e), p.h_ckpt + p.ck.e_off + row * p.ck.ld_e, (int)p.ck.ld_e, t, n);
+          } else {
+            copy_row<TH, VEC>(st + lay.at.h, p.h, row, p.rows, p.ld_h, cols, t, n);
+          }
+        }
+        if (p.y_ckpt) {
+          copy_bytes16(smem_u32(st + lay.at.y), p.y_ckpt + row * p.ck.ld_q, (int)p.ck.ld_q, t, n);
+          copy_bytes16(smem_u32(st + lay.at.y_e), p.y_ckpt + p.ck.e_off + row * p.ck.ld_e, (int)p.ck.ld_e, t, n);
+        } else if (p.y) {
+          copy_row<TY, VEC>(st + lay.at.y, p.y, row, p.rows, p.ld_y, cols, t, n);
+        }
+        if (token) copy_row<TY, VEC>(st + lay.at.gate, p.gate, row, p.rows, p.ld_gate, cols, t, n);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  // Waits for this thread's copies of the next row: a commit a row keeps the count.
+  auto arrived = [&]() {
+    if constexpr (RING) {
+      switch (lay.stages) {
+        case 2: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 5: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+      }
+    }
+  };
+
+  F8 a_post[C], a_pre[C], a_gate[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    a_post[c].fill(0.f);
+    a_pre[c].fill(0.f);
+    a_gate[c].fill(0.f);
+  }
+  F8 d[C], hv[C], yv[C];                     // of the row under way
+  F8 dl[C], yl[C];                           // w_post dn and y^ of the row before, whose dy is not written yet
+  float sum2 = 0.f, r_last = 0.f;
+
+  for (int i = 0; i < lay.stages; ++i) issue(i, i);
+  if constexpr (RING) {
+    // the first row has to be there; from then on a row's copies are waited for before the barrier of the row before
+    arrived();
+    group_sync<SOLO>(g, n);
+  }
+  int stage = 0;
+  int64_t row = row0;
+  for (int i = 0; i <= count; ++i, row += stride) {
+    const bool live = i < count;
+    const uint8_t* st = ring + stage * lay.at.bytes;
+    float sum1 = 0.f, r_pre = 0.f, r_post = 0.f;
+    if (live) {
+      if (p.pre) r_pre = p.rstd_pre[row];
+      if (p.post) r_post = p.rstd_post[row];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (p.dh_in) d[c] = take<TH, VEC, RING>(st + lay.at.dh, p.dh_in, row, p.ld_dh_in, c, t, n, cols);
+        else d[c].fill(0.f);
+        if (p.pre) {
+          if (p.h_ckpt) {
+            hv[c] = take_kept<VEC, RING>(st + lay.at.h, st + lay.at.h_e, p.h_ckpt, p.ck, row, r_pre, c, t, n);
+          } else {
+            hv[c] = take<TH, VEC, RING>(st + lay.at.h, p.h, row, p.ld_h, c, t, n, cols);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) hv[c].p[j] = mul2(hv[c].p[j], both(r_pre));
+          }
+          F8 dx = take<TY, VEC, RING>(st + lay.at.dx, p.dx, row, p.ld_dx, c, t, n, cols);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a_pre[c].p[j] = fma2(dx.p[j], hv[c].p[j], a_pre[c].p[j]);
+          if (p.w_pre) {
+            const F8 w = take_vector<VEC, RING>(RING ? vec + lay.v_pre : p.w_pre, c, t, n, cols);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dx.p[j] = mul2(dx.p[j], w.p[j]);
+          }
+          F8 part;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            part.p[j] = mul2(dx.p[j], hv[c].p[j]);
+            d[c].p[j] = fma2(both(r_pre), dx.p[j], d[c].p[j]);
+          }
+          sum1 += sum8(part);
+        }
+        if (p.y_ckpt) {
+          yv[c] = take_kept<VEC, RING>(st + lay.at.y, st + lay.at.y_e, p.y_ckpt, p.ck, row, p.post ? r_post : 1.f, c, t, n);
+        } else if (p.y) {
+          yv[c] = take<TY, VEC, RING>(st + lay.at.y, p.y, row, p.ld_y, c, t, n, cols);
+          if (p.post)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) yv[c].p[j] = mul2(yv[c].p[j], both(r_post));
+        } else {
+          yv[c].fill(0.f);
+        }
+      }
+    }
+    F8 gv[C];                                // the row's gate: its stage is given up behind the barrier
+    if (token && live)
+#pragma unroll
+      for (int c = 0; c < C; ++c) gv[c] = take<TY, VEC, RING>(st + lay.at.gate, p.gate, row, p.ld_gate, c, t, n, cols);
+    // behind this barrier every thread has read this row, and the next row's copies are there
+    arrived();
+    const float2 sums = group_sum<SOLO>(make_float2(sum1, sum2), red[i & 1], g, n, row_warps);
+    issue(i + lay.stages, stage);
+    if (RING && ++stage == lay.stages) stage = 0;
+    if (i > 0 && p.dy) {
+      TY* out = static_cast<TY*>(p.dy) + (row - stride) * p.ld_dy;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (p.post) {
+          const float2 k = both(-sums.y * inv_n);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dl[c].p[j] = mul2(both(r_last), fma2(k, yl[c].p[j], dl[c].p[j]));
+        }
+        put<VEC>(out, dl[c], c, t, n, cols);
+      }
+    }
+    if (!live) break;
+    const float2 k = both(-sums.x * inv_n * r_pre);
+    sum2 = 0.f;
+    r_last = r_post;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      F8 o;
+      if (p.pre)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[c].p[j] = fma2(k, hv[c].p[j], d[c].p[j]);
+      if (p.dh) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.p[j] = mul2(both(p.h_scale), d[c].p[j]);
+        put<VEC>(static_cast<TH*>(p.dh) + row * p.ld_dh, o, c, t, n, cols);
+      }
+      F8 w;
+      if (weighted) w = take_vector<VEC, RING>(RING ? vec + lay.v_post : p.w_post, c, t, n, cols);
+      if (CHANNEL || token) {
+        F8 value, slope;
+        if constexpr (CHANNEL && RING) {
+          value = take_vector<VEC, true>(vec + lay.v_gate, c, t, n, cols);
+          slope = take_vector<VEC, true>(vec + lay.v_slope, c, t, n, cols);
+        } else {
+          if constexpr (CHANNEL) gv[c] = take_vector<VEC, false>(static_cast<const float*>(p.gate), c, t, n, cols);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float v, sl;
+            gate_value_slope(gv[c].get(j), p.gate_act, v, sl);
+            value.set(j, p.y_scale * v);
+            slope.set(j, p.y_scale * sl * (weighted ? w.get(j) : 1.f));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 yd = mul2(yv[c].p[j], d[c].p[j]);
+          if constexpr (CHANNEL) a_gate[c].p[j] = fma2(slope.p[j], yd, a_gate[c].p[j]);
+          else o.p[j] = mul2(slope.p[j], yd);
+          d[c].p[j] = mul2(value.p[j], d[c].p[j]);
+        }
+        if (!CHANNEL && p.dgate) put<VEC>(static_cast<TY*>(p.dgate) + row * p.ld_dgate, o, c, t, n, cols);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[c].p[j] = mul2(both(p.y_scale), d[c].p[j]);
+      }
+      if (p.post) {
+        F8 part;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          a_post[c].p[j] = fma2(d[c].p[j], yv[c].p[j], a_post[c].p[j]);
+          if (weighted) d[c].p[j] = mul2(d[c].p[j], w.p[j]);
+          part.p[j] = mul2(d[c].p[j], yv[c].p[j]);
+        }
+        sum2 += sum8(part);
+      }
+      dl[c] = d[c];
+      yl[c] = yv[c];
+    }
+  }
+
+  if (!p.partial) return;
+  if constexpr (RING) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  // the block's column sums: the row groups are added in order
+  float* out = p.partial + (int64_t)blockIdx.x * 3 * cols;
+  float* fold = reinterpret_cast<float*>(dyn);
+#pragma unroll
+  for (int v = 0; v < 3; ++v) {
+    if constexpr (!SOLO) {
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < C; ++c) put<VEC>(fold + g * round4(cols), v == 0 ? a_post[c] : v == 1 ? a_pre[c] : a_gate[c], c, t, n, cols);
+      __syncthreads();
+      for (int col = threadIdx.x; col < cols; col += blockDim.x) {
+        float s = 0.f;
+        for (int i = 0; i < groups; ++i) s += fold[i * round4(cols) + col];
+        out[v * cols + col] = s;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        put<VEC>(out + v * cols, v == 0 ? a_post[c] : v == 1 ? a_pre[c] : a_gate[c], c, t, n, cols);
+    }
+  }
+}
+
+// Shared memory of a block: the vectors over the columns, then for every row group a ring of stages.
+BwdLayout layout_of(const NormParams& p, int h_bytes, int y_bytes, int64_t room) {
+  BwdLayout l{};
+  const int64_t v = round_up(p.cols, 4);
+  int64_t at = 0;
+  auto vector = [&](bool on) {
+    if (!on) return int32_t{-1};
+    at += v;
+    return (int32_t)(at - v);
+  };
+  l.v_pre = vector(p.pre && p.w_pre);
+  l.v_post = vector(p.post && p.w_post);
+  l.v_gate = vector(p.gate_kind == kGateChannel);
+  l.v_slope = vector(p.gate_kind == kGateChannel);
+  l.vectors = (int32_t)at;
+  int64_t off = 0;
+  auto slot = [&](bool on, int64_t bytes) {
+    const int64_t was = off;
+    if (on) off += round_up(bytes + 4, 16);   // a word more for rows that start inside one
+    return (int32_t)was;
+  };
+  l.at.dx = slot(p.pre, (int64_t)p.cols * y_bytes);
+  l.at.dh = slot(p.dh_in != nullptr, (int64_t)p.cols * h_bytes);
+  l.at.h = slot(p.pre, p.h_ckpt ? p.ck.ld_q : (int64_t)p.cols * h_bytes);
+  l.at.h_e = slot(p.pre && p.h_ckpt, p.ck.ld_e);
+  l.at.y = slot(p.y || p.y_ckpt, p.y_ckpt ? p.ck.ld_q : (int64_t)p.cols * y_bytes);
+  l.at.y_e = slot(p.y_ckpt != nullptr, p.ck.ld_e);
+  l.at.gate = slot(p.gate_kind == kGateToken, (int64_t)p.cols * y_bytes);
+  l.at.bytes = (int32_t)std::max<int64_t>(off, 16);
+  const int64_t ring = room - at * 4;
+  const int64_t stages = ring > 0 ? std::min<int64_t>(6, ring / (l.at.bytes * (int64_t)p.rows_per_block)) : 0;
+  l.stages = stages >= 2 ? (int32_t)stages : 0;
+  return l;
+}
+
+template <typename TH, typename TY, bool VEC, bool CHANNEL>
+int launch_c(NormParams p, int blocks, cudaStream_t s) {
+  const BwdLayout l = layout_of(p, sizeof(TH), sizeof(TY), norm_bwd_room(p));
+  if (l.stages == 0 || p.row_threads * 8 < p.cols) {   // rows too wide: 16 elements a thread, straight from memory
+    BwdLayout none{};
+    p.row_threads = (int32_t)round_up(div_up(p.cols, 16), 32);
+    return launch_kernel(norm_bwd_kernel<TH, TY, VEC, 2, 1024, true, false, CHANNEL>, dim3((unsigned)blocks),
+                         dim3((unsigned)p.row_threads), 0, s, 1, p, none);
+  }
+  const bool solo = p.rows_per_block == 1;
+  const int64_t fold = solo ? 0 : (int64_t)sizeof(float) * p.rows_per_block * round_up(p.cols, 4);
+  const int64_t smem = std::max<int64_t>(fold, l.vectors * 4 + (int64_t)l.stages * l.at.bytes * p.rows_per_block);
+  auto* k = !solo ? norm_bwd_kernel<TH, TY, VEC, 1, 256, false, true, CHANNEL>
+            : p.row_threads <= 640 ? norm_bwd_kernel<TH, TY, VEC, 1, 640, true, true, CHANNEL>
+                                   : norm_bwd_kernel<TH, TY, VEC, 1, 1024, true, true, CHANNEL>;
+  if (note_cuda_error(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+    return CZ_ERR_CUDA;
+  return launch_kernel(k, dim3((unsigned)blocks), dim3((unsigned)(p.row_threads * p.rows_per_block)), (size_t)smem, s, 1, p, l);
+}
+
+template <typename TH, typename TY>
+int launch_v(const NormParams& p, bool vec, int blocks, cudaStream_t s) {
+  if (p.gate_kind == kGateChannel)
+    return vec ? launch_c<TH, TY, true, true>(p, blocks, s) : launch_c<TH, TY, false, true>(p, blocks, s);
+  return vec ? launch_c<TH, TY, true, false>(p, blocks, s) : launch_c<TH, TY, false, false>(p, blocks, s);
+}
+
+}  // namespace
+}  // namespace cz
