@@ -53,14 +53,13 @@ bool opt_matrix_ok(const void* p, const cz_norm_args& a, int64_t ld, int64_t byt
   return p == nullptr || matrix_ok(p, a.rows, a.cols, ld, bytes);
 }
 
-// `wide`: 8 elements a thread up to 1024 threads a row.
-NormParams params_of(const cz_norm_args& a, bool wide) {
+NormParams params_of(const cz_norm_args& a, bool backward) {
   NormParams p{};
   p.rows = a.rows;
   p.cols = (int32_t)a.cols;
   // The backward holds eight fp32 values an element in registers: 8 elements a thread as long as a row
-  // fits 1024 threads.  The forward holds four: 16 a thread from 512 threads on.
-  const int64_t per = a.cols <= 8 * (wide ? 1024 : 512) ? 8 : 16;
+  // fits 1024 threads (16 on half the threads took 245 us in place of 2XX at 16384 x 5120).  The forward holds four.
+  const int64_t per = a.cols <= 8 * (backward ? 1024 : 512) ? 8 : 16;
   p.row_threads = (int32_t)round_up(div_up(a.cols, per), 32);
   p.rows_per_block = std::max(1, 256 / p.row_threads);   // narrow rows share a block of up to 8 warps
   p.post = a.post_norm;

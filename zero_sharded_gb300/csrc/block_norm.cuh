@@ -153,6 +153,7 @@ __device__ __forceinline__ void keep_chunk(uint8_t* ck, const ActLayout& l, int6
   }
 }
 
+__device__ __forceinline__ int round8(int v) { return (v + 7) & ~7; }
 __device__ __forceinline__ int round4(int v) { return (v + 3) & ~3; }
 
 }  // namespace cz

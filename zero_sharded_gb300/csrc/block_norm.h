@@ -36,7 +36,10 @@ enum { kGateNone = 0, kGateChannel = 1, kGateToken = 2 };
 
 int launch_norm_fwd(const NormParams& p, bool h_f32, bool y_f32, bool vec, void* stream);
 int launch_norm_bwd(const NormParams& p, bool h_f32, bool y_f32, bool vec, int blocks, void* stream);
+int launch_norm_bwd_bf16(const NormParams& p, bool y_f32, bool vec, int blocks, void* stream);
 int launch_norm_bwd_f32(const NormParams& p, bool y_f32, bool vec, int blocks, void* stream);
+int launch_norm_bwd_bf16_channel(const NormParams& p, bool y_f32, bool vec, int blocks, void* stream);
+int launch_norm_bwd_f32_channel(const NormParams& p, bool y_f32, bool vec, int blocks, void* stream);
 int norm_bwd_blocks_per_sm(const NormParams& p);
 int64_t norm_bwd_room(const NormParams& p);
 int launch_norm_fold(const float* partial, int blocks, int cols, float* post, float* pre, float* gate, int accumulate,

@@ -1,5 +1,8 @@
-// Backward block norms of a bf16 residual stream, and the joining of the column sums.
-#include "block_norm_bwd.cuh"
+// Backward block norms: the choice of the kernel, and the joining of the column sums.
+#include <cuda_runtime.h>
+
+#include "block_norm.h"
+#include "train_ops.h"
 
 namespace cz {
 namespace {
@@ -27,14 +30,14 @@ __global__ void __launch_bounds__(1024) norm_fold_kernel(const float* __restrict
 }  // namespace
 
 // Blocks that share an SM: two of up to 256 threads, else one.
-int norm_bwd_blocks_per_sm(const NormParams& p) { return p.row_threads * p.rows_per_block <= 320 ? 2 : 1; }
+int norm_bwd_blocks_per_sm(const NormParams& p) { return p.row_threads * p.rows_per_block <= 256 && p.cols <= 256 * 8 ? 2 : 1; }
 int64_t norm_bwd_room(const NormParams& p) { return 224 * 1024 / norm_bwd_blocks_per_sm(p) - 1024; }
 
 int launch_norm_bwd(const NormParams& p, bool h_f32, bool y_f32, bool vec, int blocks, void* stream) {
-  if (h_f32) return launch_norm_bwd_f32(p, y_f32, vec, blocks, stream);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return y_f32 ? launch_v<__nv_bfloat16, float>(p, vec, blocks, s)
-               : launch_v<__nv_bfloat16, __nv_bfloat16>(p, vec, blocks, s);
+  if (p.gate_kind == kGateChannel)
+    return h_f32 ? launch_norm_bwd_f32_channel(p, y_f32, vec, blocks, stream)
+                 : launch_norm_bwd_bf16_channel(p, y_f32, vec, blocks, stream);
+  return h_f32 ? launch_norm_bwd_f32(p, y_f32, vec, blocks, stream) : launch_norm_bwd_bf16(p, y_f32, vec, blocks, stream);
 }
 
 int launch_norm_fold(const float* partial, int blocks, int cols, float* post, float* pre, float* gate, int accumulate,

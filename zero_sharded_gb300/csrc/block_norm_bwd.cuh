@@ -14,7 +14,7 @@
 // SM has 2300 clocks for a row of 5120 columns at the memory's rate, and as many instructions as that allows.  The
 // groups' column sums are added in a fixed order by a second kernel, so results do not depend on timing.
 //
-// This file is compiled once for each type of the residual stream.
+// Compiled once for each type of the residual stream, with and without a channel gate.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -25,6 +25,8 @@
 namespace cz {
 namespace {
 
+constexpr int64_t kTimeoutClocks = 4000000000LL;   // about 2 s
+
 // A row's inputs in shared memory: byte offsets within a stage.
 struct Stage {
   int32_t dx, dh, h, h_e, y, y_e, gate, bytes;
@@ -33,10 +35,14 @@ struct Stage {
 struct BwdLayout {
   Stage at;
   int32_t stages;            // 0: rows are read from memory where they are used
+  int32_t row_bytes;         // bytes that arrive for a row
   int32_t vectors;           // floats of the vectors over the columns, which come first
   int32_t v_pre, v_post;     // w_pre, w_post; < 0: not there
   int32_t v_gate, v_slope;   // channel gate: y_scale act(gate), y_scale act'(gate) w_post
 };
+
+// Bytes of a group's ring and its barriers.
+__host__ __device__ inline int round_ring(const BwdLayout& l) { return (l.stages * (l.at.bytes + 8) + 15) / 16 * 16; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -52,14 +58,12 @@ __device__ __forceinline__ void copy_bytes16(uint32_t dst, const uint8_t* src, i
 
 // One row of a rows x cols matrix.  Rows at any alignment are copied in 4-byte words: a bf16 row that starts in the
 // middle of a word takes its neighbour's half word along, except past either end of the matrix.
-template <typename T, bool VEC>
+template <typename T>
 __device__ __forceinline__ void copy_row(uint8_t* dst, const void* base, int64_t row, int64_t rows, int64_t ld, int cols, int t,
                                          int n) {
   const T* src = static_cast<const T*>(base) + row * ld;
   const uint32_t to = smem_u32(dst);
-  if constexpr (VEC) {
-    copy_bytes16(to, reinterpret_cast<const uint8_t*>(src), cols * (int)sizeof(T), t, n);
-  } else if constexpr (sizeof(T) == 4) {
+  if constexpr (sizeof(T) == 4) {
     for (int i = t; i < cols; i += n) cp_async4(to + 4 * i, src + i, 4);
   } else {
     const int off = (int)(reinterpret_cast<uintptr_t>(src) & 2);
@@ -74,22 +78,19 @@ __device__ __forceinline__ void copy_row(uint8_t* dst, const void* base, int64_t
   }
 }
 
-// The chunk's values of a row in shared memory (RING) or in memory.
+// The chunk's values of a row in shared memory (RING) or in memory.  VEC (here and below): the chunk is in the row.
 template <typename T, bool VEC, bool RING>
 __device__ __forceinline__ F8 take(const uint8_t* stage, const void* base, int64_t row, int64_t ld, int c, int t, int n, int cols) {
   F8 v;
   if constexpr (VEC) {
     const int col = col_of<true>(c, 0, t, n);
     Raw8<T> r;
-    zero8(r);
-    if (col < cols) {
-      if constexpr (RING) {
-        const uint4* s = reinterpret_cast<const uint4*>(stage + col * (int)sizeof(T));
-        r.a = s[0];
-        if constexpr (sizeof(T) == 4) r.b = s[1];
-      } else {
-        load8(static_cast<const T*>(base) + row * ld + col, r);
-      }
+    if constexpr (RING) {
+      const uint4* s = reinterpret_cast<const uint4*>(stage + col * (int)sizeof(T));
+      r.a = s[0];
+      if constexpr (sizeof(T) == 4) r.b = s[1];
+    } else {
+      load8(static_cast<const T*>(base) + row * ld + col, r);
     }
     v = values(r);
   } else {
@@ -115,8 +116,7 @@ __device__ __forceinline__ F8 take_kept(const uint8_t* q, const uint8_t* e, cons
   }
   if constexpr (VEC) {
     const int col = col_of<true>(c, 0, t, n);
-    if (col < l.ld_q) v = act_values8(*reinterpret_cast<const uint2*>(q + col), act_scale(e[col / kActBlock]) * factor);
-    else v.fill(0.f);
+    v = act_values8(*reinterpret_cast<const uint2*>(q + col), act_scale(e[col / kActBlock]) * factor);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -127,24 +127,29 @@ __device__ __forceinline__ F8 take_kept(const uint8_t* q, const uint8_t* e, cons
   return v;
 }
 
+// Where column `col` of a vector lies in shared memory: the first and second four of every 8 columns in halves of their
+// own, so that lanes 8 columns apart read 16 bytes next to one another.
+__device__ __forceinline__ int plane_at(int col, int cols) {
+  return (col & 4 ? round8(cols) >> 1 : 0) + ((col >> 3) << 2) + (col & 3);
+}
+
 // 8 elements of a vector over the columns, in shared memory (RING) or memory.
 template <bool VEC, bool RING>
 __device__ __forceinline__ F8 take_vector(const float* w, int c, int t, int n, int cols) {
   F8 v;
   if constexpr (VEC) {
     const int col = col_of<true>(c, 0, t, n);
-    v.fill(0.f);
-    if (col < cols) {
-      if (RING || (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
-        const float4 a = *reinterpret_cast<const float4*>(w + col), b = *reinterpret_cast<const float4*>(w + col + 4);
-        v.p[0] = make_float2(a.x, a.y);
-        v.p[1] = make_float2(a.z, a.w);
-        v.p[2] = make_float2(b.x, b.y);
-        v.p[3] = make_float2(b.z, b.w);
-      } else {
+    if (RING || (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+      const float* lo = RING ? w + (col >> 1) : w + col;
+      const float* hi = RING ? lo + (round8(cols) >> 1) : lo + 4;
+      const float4 a = *reinterpret_cast<const float4*>(lo), b = *reinterpret_cast<const float4*>(hi);
+      v.p[0] = make_float2(a.x, a.y);
+      v.p[1] = make_float2(a.z, a.w);
+      v.p[2] = make_float2(b.x, b.y);
+      v.p[3] = make_float2(b.z, b.w);
+    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v.set(j, w[col + j]);
-      }
+      for (int j = 0; j < 8; ++j) v.set(j, w[col + j]);
     }
   } else {
 #pragma unroll
@@ -178,55 +183,70 @@ __device__ __forceinline__ void group_sync(int g, int n) {
   else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(n) : "memory");
 }
 
-// Sums of a and b over the threads of a row group; `red` alternates between two arrays.
-template <bool SOLO>
-__device__ __forceinline__ float2 group_sum(float2 a, float2* red, int g, int n, int row_warps) {
+// Sums of a.x and a.y over the threads of a row group; `red` alternates between two arrays.  The lower half of a
+// warp adds the first, the upper half the second, from the first exchange on.
+__device__ __forceinline__ float half_sum(float v) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1)
-    a = add2(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, d), __shfl_xor_sync(0xffffffffu, a.y, d)));
+  for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+template <bool SOLO>
+__device__ __forceinline__ float2 group_sum(float2 a, float* red, int g, int n, int row_warps) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool up = lane >= 16;
+  float v = (up ? a.y : a.x) + __shfl_xor_sync(0xffffffffu, up ? a.x : a.y, 16);
+  v = half_sum(v);
   if (row_warps == 1) {
     group_sync<SOLO>(g, n);
-    return a;
+  } else {
+    // red: the warps' first sums, then their second ones
+    if ((lane & 15) == 0) red[(up ? 32 : 0) + warp] = v;
+    group_sync<SOLO>(g, n);
+    const float* from = red + (up ? 32 : 0) + g * row_warps;
+    const int i = lane & 15;
+    v = (i < row_warps ? from[i] : 0.f) + (i + 16 < row_warps ? from[i + 16] : 0.f);
+    v = half_sum(v);
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) red[warp] = a;
-  group_sync<SOLO>(g, n);
-  a = lane < row_warps ? red[g * row_warps + lane] : make_float2(0.f, 0.f);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1)
-    a = add2(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, d), __shfl_xor_sync(0xffffffffu, a.y, d)));
-  return a;
+  return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
 }
 
-__device__ __forceinline__ float sum8(const F8& v) {
-  const float2 s = add2(add2(v.p[0], v.p[1]), add2(v.p[2], v.p[3]));
-  return s.x + s.y;
-}
+// What a kernel takes for granted, so that a row costs no tests: nothing; or both norms with weights, every gradient
+// wanted, and h' and y both as tensors or both as checkpoints.
+enum { kAny = 0, kTensors = 1, kKept = 2 };
 
 // SOLO: one row group a block.  CHANNEL: a channel gate.
-template <typename TH, typename TY, bool VEC, int C, int MAXT, bool SOLO, bool RING, bool CHANNEL>
+template <typename TH, typename TY, bool VEC, int C, int MAXT, bool SOLO, bool RING, bool CHANNEL, int MODE>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(const __grid_constant__ NormParams p,
                                                                            const __grid_constant__ BwdLayout lay) {
-  __shared__ float2 red[2][32];
+  __shared__ float red[2][64];
   extern __shared__ __align__(16) uint8_t dyn[];
   const int n = SOLO ? (int)blockDim.x : p.row_threads;
   const int g = SOLO ? 0 : threadIdx.x / n, t = threadIdx.x - g * n, row_warps = n >> 5;
   const float inv_n = 1.f / (float)p.cols;
-  const bool token = !CHANNEL && p.gate_kind == kGateToken, weighted = p.post && p.w_post;
+  const bool token = !CHANNEL && p.gate_kind == kGateToken;
+  const bool pre = MODE || p.pre, post = MODE || p.post, w_pre = MODE || (p.pre && p.w_pre), weighted = MODE || (p.post && p.w_post);
+  const bool has_dh_in = MODE || p.dh_in, has_dh = MODE || p.dh, has_dy = MODE || p.dy;
+  const bool h_kept = MODE == kKept || (MODE == kAny && p.h_ckpt), y_kept = MODE == kKept || (MODE == kAny && p.y_ckpt);
+  const bool has_y = MODE || p.y;
   const int cols = p.cols;
   float* vec = reinterpret_cast<float*>(dyn);
-  uint8_t* ring = dyn + lay.vectors * 4 + g * (lay.stages * lay.at.bytes);
+  uint8_t* ring = dyn + lay.vectors * 4 + g * round_ring(lay);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + lay.stages * lay.at.bytes);   // a barrier a stage
   if constexpr (RING) {
     for (int i = threadIdx.x; i < cols; i += blockDim.x) {
-      if (lay.v_pre >= 0) vec[lay.v_pre + i] = p.w_pre[i];
-      if (lay.v_post >= 0) vec[lay.v_post + i] = p.w_post[i];
+      const int at = VEC ? plane_at(i, cols) : i;
+      if (lay.v_pre >= 0) vec[lay.v_pre + at] = p.w_pre[i];
+      if (lay.v_post >= 0) vec[lay.v_post + at] = p.w_post[i];
       if constexpr (CHANNEL) {
         float value, slope;
         gate_value_slope(static_cast<const float*>(p.gate)[i], p.gate_act, value, slope);
-        vec[lay.v_gate + i] = p.y_scale * value;
-        vec[lay.v_slope + i] = p.y_scale * slope * (weighted ? p.w_post[i] : 1.f);
+        vec[lay.v_gate + at] = p.y_scale * value;
+        vec[lay.v_slope + at] = p.y_scale * slope * (weighted ? p.w_post[i] : 1.f);
       }
     }
+    if (VEC && t == 0)
+      for (int i = 0; i < lay.stages; ++i) mbar_init(&full[i], 1);
+    if constexpr (VEC) fence_barrier_init();
     __syncthreads();
   }
   const int groups = SOLO ? 1 : p.rows_per_block;
@@ -234,35 +254,65 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   const int64_t row0 = (int64_t)blockIdx.x * groups + g;
   const int count = row0 < p.rows ? (int)((p.rows - row0 + stride - 1) / stride) : 0;   // rows of this group
 
-  auto issue = [&](int i, int stage) {       // the copies of the group's i-th row
+  // The copies of the group's i-th row into `stage`: aligned rows as whole copies by one thread, which arrive on the
+  // stage's barrier; others in words by every thread.  The warps take turns at it.
+  int turn = 0;
+  auto issue = [&](int i, int stage) {
     if constexpr (RING) {
-      if (i < count) {
-        const int64_t row = row0 + i * stride;
-        uint8_t* st = ring + stage * lay.at.bytes;
-        if (p.pre) copy_row<TY, VEC>(st + lay.at.dx, p.dx, row, p.rows, p.ld_dx, cols, t, n);
-        if (p.dh_in) copy_row<TH, VEC>(st + lay.at.dh, p.dh_in, row, p.rows, p.ld_dh_in, cols, t, n);
-        if (p.pre) {
-          if (p.h_ckpt) {
-            copy_bytes16(smem_u32(st + lay.at.h), p.h_ckpt + row * p.ck.ld_q, (int)p.ck.ld_q, t, n);
-            copy_bytes16(smem_u32(st + lay.at.h_e), p.h_ckpt + p.ck.e_off + row * p.ck.ld_e, (int)p.ck.ld_e, t, n);
-          } else {
-            copy_row<TH, VEC>(st + lay.at.h, p.h, row, p.rows, p.ld_h, cols, t, n);
+      const int64_t row = row0 + i * stride;
+      uint8_t* st = ring + stage * lay.at.bytes;
+      if constexpr (VEC) {
+        const bool mine = t == 32 * turn;
+        if (++turn == row_warps) turn = 0;
+        if (mine && i < count) {
+          uint64_t* bar = &full[stage];
+          const uint32_t to = smem_u32(st);
+          mbar_arrive_expect_tx(bar, (uint32_t)lay.row_bytes);
+          if (p.pre) bulk_load(to + lay.at.dx, static_cast<const TY*>(p.dx) + row * p.ld_dx, cols * (int)sizeof(TY), bar);
+          if (p.dh_in) bulk_load(to + lay.at.dh, static_cast<const TH*>(p.dh_in) + row * p.ld_dh_in, cols * (int)sizeof(TH), bar);
+          if (p.pre) {
+            if (p.h_ckpt) {
+              bulk_load(to + lay.at.h, p.h_ckpt + row * p.ck.ld_q, (uint32_t)p.ck.ld_q, bar);
+              bulk_load(to + lay.at.h_e, p.h_ckpt + p.ck.e_off + row * p.ck.ld_e, (uint32_t)p.ck.ld_e, bar);
+            } else {
+              bulk_load(to + lay.at.h, static_cast<const TH*>(p.h) + row * p.ld_h, cols * (int)sizeof(TH), bar);
+            }
           }
+          if (p.y_ckpt) {
+            bulk_load(to + lay.at.y, p.y_ckpt + row * p.ck.ld_q, (uint32_t)p.ck.ld_q, bar);
+            bulk_load(to + lay.at.y_e, p.y_ckpt + p.ck.e_off + row * p.ck.ld_e, (uint32_t)p.ck.ld_e, bar);
+          } else if (p.y) {
+            bulk_load(to + lay.at.y, static_cast<const TY*>(p.y) + row * p.ld_y, cols * (int)sizeof(TY), bar);
+          }
+          if (token) bulk_load(to + lay.at.gate, static_cast<const TY*>(p.gate) + row * p.ld_gate, cols * (int)sizeof(TY), bar);
         }
-        if (p.y_ckpt) {
-          copy_bytes16(smem_u32(st + lay.at.y), p.y_ckpt + row * p.ck.ld_q, (int)p.ck.ld_q, t, n);
-          copy_bytes16(smem_u32(st + lay.at.y_e), p.y_ckpt + p.ck.e_off + row * p.ck.ld_e, (int)p.ck.ld_e, t, n);
-        } else if (p.y) {
-          copy_row<TY, VEC>(st + lay.at.y, p.y, row, p.rows, p.ld_y, cols, t, n);
+      } else {
+        if (i < count) {
+          if (p.pre) copy_row<TY>(st + lay.at.dx, p.dx, row, p.rows, p.ld_dx, cols, t, n);
+          if (p.dh_in) copy_row<TH>(st + lay.at.dh, p.dh_in, row, p.rows, p.ld_dh_in, cols, t, n);
+          if (p.pre) {
+            if (p.h_ckpt) {
+              copy_bytes16(smem_u32(st + lay.at.h), p.h_ckpt + row * p.ck.ld_q, (int)p.ck.ld_q, t, n);
+              copy_bytes16(smem_u32(st + lay.at.h_e), p.h_ckpt + p.ck.e_off + row * p.ck.ld_e, (int)p.ck.ld_e, t, n);
+            } else {
+              copy_row<TH>(st + lay.at.h, p.h, row, p.rows, p.ld_h, cols, t, n);
+            }
+          }
+          if (p.y_ckpt) {
+            copy_bytes16(smem_u32(st + lay.at.y), p.y_ckpt + row * p.ck.ld_q, (int)p.ck.ld_q, t, n);
+            copy_bytes16(smem_u32(st + lay.at.y_e), p.y_ckpt + p.ck.e_off + row * p.ck.ld_e, (int)p.ck.ld_e, t, n);
+          } else if (p.y) {
+            copy_row<TY>(st + lay.at.y, p.y, row, p.rows, p.ld_y, cols, t, n);
+          }
+          if (token) copy_row<TY>(st + lay.at.gate, p.gate, row, p.rows, p.ld_gate, cols, t, n);
         }
-        if (token) copy_row<TY, VEC>(st + lay.at.gate, p.gate, row, p.rows, p.ld_gate, cols, t, n);
+        asm volatile("cp.async.commit_group;" ::: "memory");
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     }
   };
-  // Waits for this thread's copies of the next row: a commit a row keeps the count.
+  // Word copies: waits for this thread's part of the next row (a commit a row keeps the count), before a barrier.
   auto arrived = [&]() {
-    if constexpr (RING) {
+    if constexpr (RING && !VEC) {
       switch (lay.stages) {
         case 2: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
         case 3: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
@@ -274,37 +324,59 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   };
 
   F8 a_post[C], a_pre[C], a_gate[C];
+  F8 d[C], hv[C], yv[C];                     // of the row under way
+  F8 dl[C], yl[C];                           // w_post dn and y^ of the row before, whose dy is not written yet
+  bool in[C];                                // aligned rows: a chunk is in the row or not
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     a_post[c].fill(0.f);
     a_pre[c].fill(0.f);
     a_gate[c].fill(0.f);
+    d[c].fill(0.f);
+    hv[c].fill(0.f);
+    yv[c].fill(0.f);
+    in[c] = !VEC || col_of<VEC>(c, 0, t, n) < cols;
   }
-  F8 d[C], hv[C], yv[C];                     // of the row under way
-  F8 dl[C], yl[C];                           // w_post dn and y^ of the row before, whose dy is not written yet
   float sum2 = 0.f, r_last = 0.f;
 
   for (int i = 0; i < lay.stages; ++i) issue(i, i);
-  if constexpr (RING) {
+  if constexpr (RING && !VEC) {
     // the first row has to be there; from then on a row's copies are waited for before the barrier of the row before
     arrived();
     group_sync<SOLO>(g, n);
   }
   int stage = 0;
+  uint32_t phase = 0;
   int64_t row = row0;
-  for (int i = 0; i <= count; ++i, row += stride) {
+  TH* out_h = static_cast<TH*>(p.dh) + row * p.ld_dh;
+  TY* out_y = static_cast<TY*>(p.dy) + (row - stride) * p.ld_dy;   // of the row before
+  const int64_t step_h = stride * p.ld_dh, step_y = stride * p.ld_dy;
+  float next_pre = 0.f, next_post = 0.f;     // a row's factors are loaded a row ahead
+  if (count > 0) {
+    if (pre) next_pre = p.rstd_pre[row];
+    if (post) next_post = p.rstd_post[row];
+  }
+  for (int i = 0; i <= count; ++i, row += stride, out_h += step_h, out_y += step_y) {
     const bool live = i < count;
     const uint8_t* st = ring + stage * lay.at.bytes;
-    float sum1 = 0.f, r_pre = 0.f, r_post = 0.f;
+    float sum1 = 0.f;
+    const float r_pre = next_pre, r_post = next_post;
+    F8 gv[C];                                // the row's gate: its stage is given up behind the barrier
     if (live) {
-      if (p.pre) r_pre = p.rstd_pre[row];
-      if (p.post) r_post = p.rstd_post[row];
+      if (i + 1 < count) {
+        if (pre) next_pre = p.rstd_pre[row + stride];
+        if (post) next_post = p.rstd_post[row + stride];
+      }
+      // a copy that never arrives shows as NaN in the row and in the column sums
+      const bool there = !(RING && VEC) || mbar_poll(&full[stage], phase, nullptr, nullptr, kTimeoutClocks);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (p.dh_in) d[c] = take<TH, VEC, RING>(st + lay.at.dh, p.dh_in, row, p.ld_dh_in, c, t, n, cols);
+        if (!in[c]) continue;
+        if (has_dh_in) d[c] = take<TH, VEC, RING>(st + lay.at.dh, p.dh_in, row, p.ld_dh_in, c, t, n, cols);
         else d[c].fill(0.f);
-        if (p.pre) {
-          if (p.h_ckpt) {
+        if (!there) d[c].fill(__uint_as_float(0x7FC00000u));
+        if (pre) {
+          if (h_kept) {
             hv[c] = take_kept<VEC, RING>(st + lay.at.h, st + lay.at.h_e, p.h_ckpt, p.ck, row, r_pre, c, t, n);
           } else {
             hv[c] = take<TH, VEC, RING>(st + lay.at.h, p.h, row, p.ld_h, c, t, n, cols);
@@ -314,50 +386,47 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
           F8 dx = take<TY, VEC, RING>(st + lay.at.dx, p.dx, row, p.ld_dx, c, t, n, cols);
 #pragma unroll
           for (int j = 0; j < 4; ++j) a_pre[c].p[j] = fma2(dx.p[j], hv[c].p[j], a_pre[c].p[j]);
-          if (p.w_pre) {
+          if (w_pre) {
             const F8 w = take_vector<VEC, RING>(RING ? vec + lay.v_pre : p.w_pre, c, t, n, cols);
 #pragma unroll
             for (int j = 0; j < 4; ++j) dx.p[j] = mul2(dx.p[j], w.p[j]);
           }
-          F8 part;
+          float2 part = make_float2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            part.p[j] = mul2(dx.p[j], hv[c].p[j]);
+            part = fma2(dx.p[j], hv[c].p[j], part);
             d[c].p[j] = fma2(both(r_pre), dx.p[j], d[c].p[j]);
           }
-          sum1 += sum8(part);
+          sum1 += part.x + part.y;
         }
-        if (p.y_ckpt) {
-          yv[c] = take_kept<VEC, RING>(st + lay.at.y, st + lay.at.y_e, p.y_ckpt, p.ck, row, p.post ? r_post : 1.f, c, t, n);
-        } else if (p.y) {
+        if (y_kept) {
+          yv[c] = take_kept<VEC, RING>(st + lay.at.y, st + lay.at.y_e, p.y_ckpt, p.ck, row, post ? r_post : 1.f, c, t, n);
+        } else if (has_y) {
           yv[c] = take<TY, VEC, RING>(st + lay.at.y, p.y, row, p.ld_y, c, t, n, cols);
-          if (p.post)
+          if (post)
 #pragma unroll
             for (int j = 0; j < 4; ++j) yv[c].p[j] = mul2(yv[c].p[j], both(r_post));
-        } else {
-          yv[c].fill(0.f);
         }
+        if (token) gv[c] = take<TY, VEC, RING>(st + lay.at.gate, p.gate, row, p.ld_gate, c, t, n, cols);
       }
     }
-    F8 gv[C];                                // the row's gate: its stage is given up behind the barrier
-    if (token && live)
-#pragma unroll
-      for (int c = 0; c < C; ++c) gv[c] = take<TY, VEC, RING>(st + lay.at.gate, p.gate, row, p.ld_gate, c, t, n, cols);
-    // behind this barrier every thread has read this row, and the next row's copies are there
+    // behind this barrier every thread has read this row, and (word copies) the next row's are there
     arrived();
     const float2 sums = group_sum<SOLO>(make_float2(sum1, sum2), red[i & 1], g, n, row_warps);
     issue(i + lay.stages, stage);
-    if (RING && ++stage == lay.stages) stage = 0;
-    if (i > 0 && p.dy) {
-      TY* out = static_cast<TY*>(p.dy) + (row - stride) * p.ld_dy;
+    if (RING && ++stage == lay.stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    if (i > 0 && has_dy) {
+      const float2 k = both(-sums.y * inv_n), r = both(r_last);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (p.post) {
-          const float2 k = both(-sums.y * inv_n);
+        if (!in[c]) continue;
+        if (post)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) dl[c].p[j] = mul2(both(r_last), fma2(k, yl[c].p[j], dl[c].p[j]));
-        }
-        put<VEC>(out, dl[c], c, t, n, cols);
+          for (int j = 0; j < 4; ++j) dl[c].p[j] = mul2(r, fma2(k, yl[c].p[j], dl[c].p[j]));
+        put<VEC>(out_y, dl[c], c, t, n, cols);
       }
     }
     if (!live) break;
@@ -366,14 +435,15 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
     r_last = r_post;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
+      if (!in[c]) continue;
       F8 o;
-      if (p.pre)
+      if (pre)
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[c].p[j] = fma2(k, hv[c].p[j], d[c].p[j]);
-      if (p.dh) {
+      if (has_dh) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) o.p[j] = mul2(both(p.h_scale), d[c].p[j]);
-        put<VEC>(static_cast<TH*>(p.dh) + row * p.ld_dh, o, c, t, n, cols);
+        put<VEC>(out_h, o, c, t, n, cols);
       }
       F8 w;
       if (weighted) w = take_vector<VEC, RING>(RING ? vec + lay.v_post : p.w_post, c, t, n, cols);
@@ -404,15 +474,15 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[c].p[j] = mul2(both(p.y_scale), d[c].p[j]);
       }
-      if (p.post) {
-        F8 part;
+      if (post) {
+        float2 part = make_float2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           a_post[c].p[j] = fma2(d[c].p[j], yv[c].p[j], a_post[c].p[j]);
           if (weighted) d[c].p[j] = mul2(d[c].p[j], w.p[j]);
-          part.p[j] = mul2(d[c].p[j], yv[c].p[j]);
+          part = fma2(d[c].p[j], yv[c].p[j], part);
         }
-        sum2 += sum8(part);
+        sum2 += part.x + part.y;
       }
       dl[c] = d[c];
       yl[c] = yv[c];
@@ -420,7 +490,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   }
 
   if (!p.partial) return;
-  if constexpr (RING) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if constexpr (RING && !VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
   // the block's column sums: the row groups are added in order
   float* out = p.partial + (int64_t)blockIdx.x * 3 * cols;
   float* fold = reinterpret_cast<float*>(dyn);
@@ -447,7 +517,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
 // Shared memory of a block: the vectors over the columns, then for every row group a ring of stages.
 BwdLayout layout_of(const NormParams& p, int h_bytes, int y_bytes, int64_t room) {
   BwdLayout l{};
-  const int64_t v = round_up(p.cols, 4);
+  const int64_t v = round_up(p.cols, 8);
   int64_t at = 0;
   auto vector = [&](bool on) {
     if (!on) return int32_t{-1};
@@ -462,7 +532,10 @@ BwdLayout layout_of(const NormParams& p, int h_bytes, int y_bytes, int64_t room)
   int64_t off = 0;
   auto slot = [&](bool on, int64_t bytes) {
     const int64_t was = off;
-    if (on) off += round_up(bytes + 4, 16);   // a word more for rows that start inside one
+    if (on) {
+      off += round_up(bytes + 4, 16);         // a word more for rows that start inside one
+      l.row_bytes += (int32_t)bytes;
+    }
     return (int32_t)was;
   };
   l.at.dx = slot(p.pre, (int64_t)p.cols * y_bytes);
@@ -474,36 +547,49 @@ BwdLayout layout_of(const NormParams& p, int h_bytes, int y_bytes, int64_t room)
   l.at.gate = slot(p.gate_kind == kGateToken, (int64_t)p.cols * y_bytes);
   l.at.bytes = (int32_t)std::max<int64_t>(off, 16);
   const int64_t ring = room - at * 4;
-  const int64_t stages = ring > 0 ? std::min<int64_t>(6, ring / (l.at.bytes * (int64_t)p.rows_per_block)) : 0;
+  const int64_t stages = ring > 0 ? std::min<int64_t>(6, ring / ((l.at.bytes + 16) * (int64_t)p.rows_per_block)) : 0;
   l.stages = stages >= 2 ? (int32_t)stages : 0;
   return l;
 }
 
-template <typename TH, typename TY, bool VEC, bool CHANNEL>
-int launch_c(NormParams p, int blocks, cudaStream_t s) {
-  const BwdLayout l = layout_of(p, sizeof(TH), sizeof(TY), norm_bwd_room(p));
-  if (l.stages == 0 || p.row_threads * 8 < p.cols) {   // rows too wide: 16 elements a thread, straight from memory
-    BwdLayout none{};
-    p.row_threads = (int32_t)round_up(div_up(p.cols, 16), 32);
-    return launch_kernel(norm_bwd_kernel<TH, TY, VEC, 2, 1024, true, false, CHANNEL>, dim3((unsigned)blocks),
-                         dim3((unsigned)p.row_threads), 0, s, 1, p, none);
-  }
+template <typename TH, typename TY, bool VEC, bool CHANNEL, int MODE>
+int launch_ring(const NormParams& p, const BwdLayout& l, int blocks, cudaStream_t s) {
   const bool solo = p.rows_per_block == 1;
   const int64_t fold = solo ? 0 : (int64_t)sizeof(float) * p.rows_per_block * round_up(p.cols, 4);
-  const int64_t smem = std::max<int64_t>(fold, l.vectors * 4 + (int64_t)l.stages * l.at.bytes * p.rows_per_block);
-  auto* k = !solo ? norm_bwd_kernel<TH, TY, VEC, 1, 256, false, true, CHANNEL>
-            : p.row_threads <= 640 ? norm_bwd_kernel<TH, TY, VEC, 1, 640, true, true, CHANNEL>
-                                   : norm_bwd_kernel<TH, TY, VEC, 1, 1024, true, true, CHANNEL>;
+  const int64_t smem = std::max<int64_t>(fold, l.vectors * 4 + (int64_t)round_ring(l) * p.rows_per_block);
+  auto* k = !solo ? norm_bwd_kernel<TH, TY, VEC, 1, 256, false, true, CHANNEL, MODE>
+            : p.row_threads > 256 && p.row_threads <= 640 ? norm_bwd_kernel<TH, TY, VEC, 1, 640, true, true, CHANNEL, MODE>
+            : p.row_threads <= 256 ? norm_bwd_kernel<TH, TY, VEC, 1, 256, true, true, CHANNEL, MODE>
+                                   : norm_bwd_kernel<TH, TY, VEC, 1, 1024, true, true, CHANNEL, MODE>;
   if (note_cuda_error(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
     return CZ_ERR_CUDA;
   return launch_kernel(k, dim3((unsigned)blocks), dim3((unsigned)(p.row_threads * p.rows_per_block)), (size_t)smem, s, 1, p, l);
 }
 
-template <typename TH, typename TY>
-int launch_v(const NormParams& p, bool vec, int blocks, cudaStream_t s) {
-  if (p.gate_kind == kGateChannel)
-    return vec ? launch_c<TH, TY, true, true>(p, blocks, s) : launch_c<TH, TY, false, true>(p, blocks, s);
-  return vec ? launch_c<TH, TY, true, false>(p, blocks, s) : launch_c<TH, TY, false, false>(p, blocks, s);
+template <typename TH, typename TY, bool VEC, bool CHANNEL>
+int launch_c(NormParams p, int blocks, cudaStream_t s) {
+  const BwdLayout l = layout_of(p, sizeof(TH), sizeof(TY), norm_bwd_room(p));
+  if (l.stages == 0 || p.cols > 8 * 1024) {   // rows too wide: 16 elements a thread, straight from memory
+    BwdLayout none{};
+    p.row_threads = (int32_t)round_up(div_up(p.cols, 16), 32);
+    return launch_kernel(norm_bwd_kernel<TH, TY, VEC, 2, 1024, true, false, CHANNEL, kAny>, dim3((unsigned)blocks),
+                         dim3((unsigned)p.row_threads), 0, s, 1, p, none);
+  }
+  // the tests that kTensors and kKept save are worth their kernels for aligned bf16 activations
+  if constexpr (VEC && sizeof(TY) == 2) {
+    if (p.pre && p.post && p.w_pre && p.w_post && p.dh_in && p.dh && p.dy && (p.gate_kind != kGateToken || p.dgate)) {
+      if (p.h_ckpt && p.y_ckpt) return launch_ring<TH, TY, VEC, CHANNEL, kKept>(p, l, blocks, s);
+      if (!p.h_ckpt && !p.y_ckpt) return launch_ring<TH, TY, VEC, CHANNEL, kTensors>(p, l, blocks, s);
+    }
+  }
+  return launch_ring<TH, TY, VEC, CHANNEL, kAny>(p, l, blocks, s);
+}
+
+template <typename TH, bool CHANNEL>
+int launch_y(const NormParams& p, bool y_f32, bool vec, int blocks, void* stream) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (y_f32) return vec ? launch_c<TH, float, true, CHANNEL>(p, blocks, s) : launch_c<TH, float, false, CHANNEL>(p, blocks, s);
+  return vec ? launch_c<TH, __nv_bfloat16, true, CHANNEL>(p, blocks, s) : launch_c<TH, __nv_bfloat16, false, CHANNEL>(p, blocks, s);
 }
 
 }  // namespace

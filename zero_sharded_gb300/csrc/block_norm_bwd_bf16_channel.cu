@@ -1,0 +1,10 @@
+// Backward block norms of a bf16 residual stream, with a channel gate.
+#include "block_norm_bwd.cuh"
+
+namespace cz {
+
+int launch_norm_bwd_bf16_channel(const NormParams& p, bool y_f32, bool vec, int blocks, void* stream) {
+  return launch_y<__nv_bfloat16, true>(p, y_f32, vec, blocks, stream);
+}
+
+}  // namespace cz
