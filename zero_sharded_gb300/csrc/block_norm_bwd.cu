@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(1024) norm_fold_kernel(const float* __restrict
 
 // Blocks that share an SM: two of up to 256 threads, else one.
 int norm_bwd_blocks_per_sm(const NormParams& p) { return p.row_threads * p.rows_per_block <= 256 && p.cols <= 256 * 8 ? 2 : 1; }
-int64_t norm_bwd_room(const NormParams& p) { return 224 * 1024 / norm_bwd_blocks_per_sm(p) - 1024; }
+int64_t norm_bwd_room(const NormParams& p) { return 222 * 1024 / norm_bwd_blocks_per_sm(p) - 6 * 1024; }
 
 int launch_norm_bwd(const NormParams& p, bool h_f32, bool y_f32, bool vec, int blocks, void* stream) {
   if (p.gate_kind == kGateChannel)

@@ -26,6 +26,7 @@ namespace cz {
 namespace {
 
 constexpr int64_t kTimeoutClocks = 4000000000LL;   // about 2 s
+constexpr int kFactors = 64;                       // rows whose r_h and r_y are loaded together
 
 // A row's inputs in shared memory: byte offsets within a stage.
 struct Stage {
@@ -176,10 +177,8 @@ __device__ __forceinline__ void put(T* row, const F8& v, int c, int t, int n, in
 }
 
 // Barrier of the n threads of row group g.
-template <bool SOLO>
 __device__ __forceinline__ void group_sync(int g, int n) {
-  if constexpr (SOLO) __syncthreads();
-  else if (n == 32) __syncwarp();
+  if (n == 32) __syncwarp();
   else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(n) : "memory");
 }
 
@@ -190,18 +189,17 @@ __device__ __forceinline__ float half_sum(float v) {
   for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
 }
-template <bool SOLO>
 __device__ __forceinline__ float2 group_sum(float2 a, float* red, int g, int n, int row_warps) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool up = lane >= 16;
   float v = (up ? a.y : a.x) + __shfl_xor_sync(0xffffffffu, up ? a.x : a.y, 16);
   v = half_sum(v);
   if (row_warps == 1) {
-    group_sync<SOLO>(g, n);
+    group_sync(g, n);
   } else {
     // red: the warps' first sums, then their second ones
     if ((lane & 15) == 0) red[(up ? 32 : 0) + warp] = v;
-    group_sync<SOLO>(g, n);
+    group_sync(g, n);
     const float* from = red + (up ? 32 : 0) + g * row_warps;
     const int i = lane & 15;
     v = (i < row_warps ? from[i] : 0.f) + (i + 16 < row_warps ? from[i + 16] : 0.f);
@@ -220,7 +218,9 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
                                                                            const __grid_constant__ BwdLayout lay) {
   __shared__ float red[2][64];
   extern __shared__ __align__(16) uint8_t dyn[];
+  constexpr bool BULK = RING && VEC;
   const int n = SOLO ? (int)blockDim.x : p.row_threads;
+  const int groups = SOLO ? 1 : p.rows_per_block;
   const int g = SOLO ? 0 : threadIdx.x / n, t = threadIdx.x - g * n, row_warps = n >> 5;
   const float inv_n = 1.f / (float)p.cols;
   const bool token = !CHANNEL && p.gate_kind == kGateToken;
@@ -231,7 +231,9 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   const int cols = p.cols;
   float* vec = reinterpret_cast<float*>(dyn);
   uint8_t* ring = dyn + lay.vectors * 4 + g * round_ring(lay);
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + lay.stages * lay.at.bytes);   // a barrier a stage
+  // behind the stages a barrier each
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + lay.stages * lay.at.bytes);
+  __shared__ float factors[SOLO ? 1 : 8][2][kFactors];
   if constexpr (RING) {
     for (int i = threadIdx.x; i < cols; i += blockDim.x) {
       const int at = VEC ? plane_at(i, cols) : i;
@@ -244,18 +246,18 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
         vec[lay.v_slope + at] = p.y_scale * slope * (weighted ? p.w_post[i] : 1.f);
       }
     }
-    if (VEC && t == 0)
+    if (VEC && t == 0) {
       for (int i = 0; i < lay.stages; ++i) mbar_init(&full[i], 1);
-    if constexpr (VEC) fence_barrier_init();
+      fence_barrier_init();
+    }
     __syncthreads();
   }
-  const int groups = SOLO ? 1 : p.rows_per_block;
   const int64_t stride = (int64_t)gridDim.x * groups;
   const int64_t row0 = (int64_t)blockIdx.x * groups + g;
   const int count = row0 < p.rows ? (int)((p.rows - row0 + stride - 1) / stride) : 0;   // rows of this group
 
-  // The copies of the group's i-th row into `stage`: aligned rows as whole copies by one thread, which arrive on the
-  // stage's barrier; others in words by every thread.  The warps take turns at it.
+  // The copies of the group's i-th row into `stage`: aligned rows as whole copies by one thread (the warps take
+  // turns), which arrive on the stage's barrier; others in words by every thread.
   int turn = 0;
   auto issue = [&](int i, int stage) {
     if constexpr (RING) {
@@ -268,20 +270,20 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
           uint64_t* bar = &full[stage];
           const uint32_t to = smem_u32(st);
           mbar_arrive_expect_tx(bar, (uint32_t)lay.row_bytes);
-          if (p.pre) bulk_load(to + lay.at.dx, static_cast<const TY*>(p.dx) + row * p.ld_dx, cols * (int)sizeof(TY), bar);
-          if (p.dh_in) bulk_load(to + lay.at.dh, static_cast<const TH*>(p.dh_in) + row * p.ld_dh_in, cols * (int)sizeof(TH), bar);
-          if (p.pre) {
-            if (p.h_ckpt) {
+          if (pre) bulk_load(to + lay.at.dx, static_cast<const TY*>(p.dx) + row * p.ld_dx, cols * (int)sizeof(TY), bar);
+          if (has_dh_in) bulk_load(to + lay.at.dh, static_cast<const TH*>(p.dh_in) + row * p.ld_dh_in, cols * (int)sizeof(TH), bar);
+          if (pre) {
+            if (h_kept) {
               bulk_load(to + lay.at.h, p.h_ckpt + row * p.ck.ld_q, (uint32_t)p.ck.ld_q, bar);
               bulk_load(to + lay.at.h_e, p.h_ckpt + p.ck.e_off + row * p.ck.ld_e, (uint32_t)p.ck.ld_e, bar);
             } else {
               bulk_load(to + lay.at.h, static_cast<const TH*>(p.h) + row * p.ld_h, cols * (int)sizeof(TH), bar);
             }
           }
-          if (p.y_ckpt) {
+          if (y_kept) {
             bulk_load(to + lay.at.y, p.y_ckpt + row * p.ck.ld_q, (uint32_t)p.ck.ld_q, bar);
             bulk_load(to + lay.at.y_e, p.y_ckpt + p.ck.e_off + row * p.ck.ld_e, (uint32_t)p.ck.ld_e, bar);
-          } else if (p.y) {
+          } else if (has_y) {
             bulk_load(to + lay.at.y, static_cast<const TY*>(p.y) + row * p.ld_y, cols * (int)sizeof(TY), bar);
           }
           if (token) bulk_load(to + lay.at.gate, static_cast<const TY*>(p.gate) + row * p.ld_gate, cols * (int)sizeof(TY), bar);
@@ -343,32 +345,36 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   if constexpr (RING && !VEC) {
     // the first row has to be there; from then on a row's copies are waited for before the barrier of the row before
     arrived();
-    group_sync<SOLO>(g, n);
+    group_sync(g, n);
   }
   int stage = 0;
   uint32_t phase = 0;
+  bool there = true;
   int64_t row = row0;
   TH* out_h = static_cast<TH*>(p.dh) + row * p.ld_dh;
   TY* out_y = static_cast<TY*>(p.dy) + (row - stride) * p.ld_dy;   // of the row before
   const int64_t step_h = stride * p.ld_dh, step_y = stride * p.ld_dy;
-  float next_pre = 0.f, next_post = 0.f;     // a row's factors are loaded a row ahead
-  if (count > 0) {
-    if (pre) next_pre = p.rstd_pre[row];
-    if (post) next_post = p.rstd_post[row];
-  }
   for (int i = 0; i <= count; ++i, row += stride, out_h += step_h, out_y += step_y) {
     const bool live = i < count;
     const uint8_t* st = ring + stage * lay.at.bytes;
     float sum1 = 0.f;
-    const float r_pre = next_pre, r_post = next_post;
+    float r_pre = 0.f, r_post = 0.f;
     F8 gv[C];                                // the row's gate: its stage is given up behind the barrier
     if (live) {
-      if (i + 1 < count) {
-        if (pre) next_pre = p.rstd_pre[row + stride];
-        if (post) next_post = p.rstd_post[row + stride];
+      // the factors of kFactors rows at a time: loaded row by row they held up every row by their latency
+      const int f = i & (kFactors - 1);
+      if (f == 0) {
+        if (i > 0) group_sync(g, n);
+        for (int j = t; j < kFactors && i + j < count; j += n) {
+          factors[g][0][j] = pre ? p.rstd_pre[row + j * stride] : 0.f;
+          factors[g][1][j] = post ? p.rstd_post[row + j * stride] : 0.f;
+        }
+        group_sync(g, n);
       }
+      r_pre = factors[g][0][f];
+      r_post = factors[g][1][f];
       // a copy that never arrives shows as NaN in the row and in the column sums
-      const bool there = !(RING && VEC) || mbar_poll(&full[stage], phase, nullptr, nullptr, kTimeoutClocks);
+      there = there && (!BULK || mbar_poll(&full[stage], phase, nullptr, nullptr, kTimeoutClocks));
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         if (!in[c]) continue;
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
     }
     // behind this barrier every thread has read this row, and (word copies) the next row's are there
     arrived();
-    const float2 sums = group_sum<SOLO>(make_float2(sum1, sum2), red[i & 1], g, n, row_warps);
+    const float2 sums = group_sum(make_float2(sum1, sum2), red[i & 1], g, n, row_warps);
     issue(i + lay.stages, stage);
     if (RING && ++stage == lay.stages) {
       stage = 0;
