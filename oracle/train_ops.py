@@ -118,6 +118,12 @@ def _z(x, inv_temp):
     return np.where(z < -most, -np.inf, np.where(z > most, np.inf, z))
 
 
+def _log_p(z):
+    """Log probabilities from the distance to the maximum (z - lse would lose the sum beside a large maximum)."""
+    d = z - z.max()
+    return d - np.log(np.exp(d).sum())
+
+
 def logp_fwd(logits, targets, inv_temp=1.0, top_k=0) -> dict:
     """Rows of nothing but masked entries (-inf or a type's lowest value): lse -inf, logp -inf (0 without a target), entropy 0, top log probabilities -inf."""
     x = np.asarray(logits, np.float64)
@@ -133,9 +139,8 @@ def logp_fwd(logits, targets, inv_temp=1.0, top_k=0) -> dict:
         elif x[r].max() <= -1e37 or (z == -np.inf).all():
             lse, entropy, lp = -np.inf, 0.0, np.full(vocab, -np.inf)
         else:
-            m = z.max()
-            lse = m + np.log(np.exp(z - m).sum())
-            lp = z - lse
+            lp = _log_p(z)
+            lse = z.max() + np.log(np.exp(z - z.max()).sum())
             p = np.exp(lp)
             entropy = -(p[p > 0] * lp[p > 0]).sum()
         out["lse"][r], out["entropy"][r] = lse, entropy
@@ -154,7 +159,7 @@ def logp_bwd(logits, targets, g_logp=None, g_entropy=None, inv_temp=1.0) -> np.n
         if f["lse"][r] == -np.inf:
             continue
         t = int(targets[r])
-        lp = _z(x[r], inv_temp) - f["lse"][r]
+        lp = _log_p(_z(x[r], inv_temp))
         p = np.exp(lp)
         if g_logp is not None and t >= 0:
             if t >= x.shape[1]:

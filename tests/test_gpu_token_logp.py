@@ -104,6 +104,23 @@ def test_masked_empty_and_special_rows(vocab, dtype, inv_temp):
     assert bool((d[4] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("at", [3e4, -3e4, 1e30, -1e30, 3e38])
+def test_rows_of_large_values(at, dtype):
+    """Rows whose values differ by less than their size: spacing of the type around a large maximum, with masked entries
+    of both kinds and a part of nothing but masks."""
+    vocab = 70001
+    x, t = _logits(4, vocab, 12, 3.0)
+    x = (x * abs(at) * 2.0 ** -7).clamp(-0.4 * abs(at), 0.0) + at
+    x[1, ::3] = -float("inf")
+    x[2, vocab // 3:] = torch.finfo(TYPES[dtype]).min
+    x[2, vocab // 2::2] = -float("inf")
+    x[3, 4096:] = -float("inf")
+    t[2], t[3] = 0, 1
+    t[1] = 1
+    _check_forward(x.to(TYPES[dtype]).cuda(), t.cuda(), 1.0, 20)
+
+
 @pytest.mark.parametrize("shape", ["ascending", "one thread's part", "sorted blocks"])
 def test_alternatives_of_skewed_rows(shape):
     """Rows that put forward more candidates than the buffer holds."""

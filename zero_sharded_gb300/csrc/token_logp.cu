@@ -3,14 +3,15 @@
 // Forward, z = x inv_temp, m = max x, c = inv_temp log2(e), d_j = (x_j - m) c:
 //   s = sum 2^d_j,  w = sum 2^d_j d_j,  lse = m inv_temp + ln s,  entropy = ln s - ln2 w / s
 // in one pass over the row: every thread keeps (m, s, w) of the elements it has seen and
-// rescales s and w when its maximum grows; the threads', warps' and cluster blocks'
+// rescales s and w when the maximum of the next vectors exceeds m; the threads', warps' and cluster blocks'
 // triples are joined in a fixed order.  x - m is formed before the scale, so that rows of a
-// type's lowest value and masked -inf entries stay finite; d is held to >= -150, where
-// 2^d is 0, so that a masked entry's 2^d d is 0 and not NaN.
+// type's lowest value and masked -inf entries stay finite; x is held to >= m - 150 / c, where 2^d
+// is 0, so that a masked entry's 2^d d is 0 and not NaN.  Maxima of bf16 are taken before unpacking and
+// the rest runs on pairs: five instructions an element, where memory leaves time for eight.
 //
-// Top alternatives cost no second pass: the k-th largest of the maxima of groups of 8
-// threads (disjoint parts of the row) is a bound that the k largest elements reach, so only threads whose
-// own maximum reaches it read their part again and put forward what does.  Keys of (value,
+// Top alternatives cost no second pass: the k-th largest of the maxima of groups of 4
+// threads (disjoint parts of the row) is a bound that the k largest elements reach, so only the parts of threads
+// whose own maximum reaches it are read again, each by a whole warp.  Keys of (value,
 // complement of the index) make the order total.  Should ties or a skewed row
 // put forward more than the buffer holds, k rounds of a block-wide maximum below the last
 // key find them instead.
@@ -26,25 +27,53 @@
 namespace cz {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroups = kWarps * 4;       // groups of 8 threads
+constexpr int kGroups = kThreads / 4;     // groups of 4 threads
+static_assert(kGroups == 64, "two groups a lane");
 constexpr int kCand = 1024;               // candidates that the buffer holds
 constexpr float kMasked = -1e37f;         // a largest logit below this: -inf or a type's lowest value throughout
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 static_assert(kGroups >= CZ_LOGP_MAX_TOP, "the bound needs top_k groups");
+
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 template <typename T>
 struct Vec;                                // 16 bytes of elements
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
+  using Floor = uint32_t;                  // a lower bound for the elements, twice
+  static constexpr float kLowest = -3.3895313892515355e38f;
   __device__ static void values(uint4 r, float* v) { unpack8(r, v); }
   __device__ static uint4 pack(const float* v) { return pack8(v); }
+  __device__ static Floor floor_of(float f) { return pack_bf16x2(f, f); }
+  __device__ static uint4 hold(uint4 r, Floor f) {
+    return make_uint4(max_nan_bf16x2(r.x, f), max_nan_bf16x2(r.y, f), max_nan_bf16x2(r.z, f), max_nan_bf16x2(r.w, f));
+  }
+  // The larger of two vectors element by element, and the largest element.
+  __device__ static uint4 larger(uint4 a, uint4 b) {
+    return make_uint4(max_nan_bf16x2(a.x, b.x), max_nan_bf16x2(a.y, b.y), max_nan_bf16x2(a.z, b.z), max_nan_bf16x2(a.w, b.w));
+  }
+  __device__ static float largest(uint4 r) {
+    const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(r.x, r.y), max_nan_bf16x2(r.z, r.w));
+    return max_nan(bf16_lo(m), bf16_hi(m));
+  }
 };
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
+  using Floor = float;
+  static constexpr float kLowest = -3.4028234663852886e38f;
   __device__ static void values(uint4 r, float* v) {
     v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y);
     v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
@@ -52,13 +81,16 @@ struct Vec<float> {
   __device__ static uint4 pack(const float* v) {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
   }
+  __device__ static uint32_t one(uint32_t a, uint32_t b) { return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b))); }
+  __device__ static Floor floor_of(float f) { return f; }
+  __device__ static uint4 larger(uint4 a, uint4 b) { return make_uint4(one(a.x, b.x), one(a.y, b.y), one(a.z, b.z), one(a.w, b.w)); }
+  __device__ static uint4 hold(uint4 r, Floor f) {
+    const uint32_t u = __float_as_uint(f);
+    return larger(r, make_uint4(u, u, u, u));
+  }
+  __device__ static float largest(uint4 r) { return __uint_as_float(one(one(r.x, r.y), one(r.z, r.w))); }
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -149,8 +181,8 @@ __device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float g = own_max;
 #pragma unroll
-  for (int d = 1; d < 8; d <<= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, d));
-  if ((lane & 7) == 0) sh.group[warp * 4 + (lane >> 3)] = g;
+  for (int d = 1; d < 4; d <<= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, d));
+  if ((lane & 3) == 0) sh.group[warp * 8 + (lane >> 2)] = g;
   if (threadIdx.x == 0) sh.n_cand = 0;
   if ((int)threadIdx.x < k) sh.top[threadIdx.x] = 0;
   __syncthreads();
@@ -167,13 +199,25 @@ __device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool 
   const uint32_t ha = __ballot_sync(0xffffffffu, ra == k - 1), hb = __ballot_sync(0xffffffffu, rb == k - 1);
   const float bound = ha ? __shfl_sync(0xffffffffu, ga, __ffs(ha) - 1) : __shfl_sync(0xffffffffu, gb, max(__ffs(hb) - 1, 0));
   if (!nan) {
-    if (own_max >= bound)
-      each(r, v0, v1, singles, [&](float x, uint32_t i) {
-        if (x >= bound) {
-          const int at = atomicAdd(&sh.n_cand, 1);
-          if (at < kCand) sh.cand[at] = key_of(x, i);
-        }
-      });
+    auto put_forward = [&](float x, uint32_t i) {
+      if (x >= bound) {
+        const int at = atomicAdd(&sh.n_cand, 1);
+        if (at < kCand) sh.cand[at] = key_of(x, i);
+      }
+    };
+    for (uint32_t todo = __ballot_sync(0xffffffffu, own_max >= bound); todo; todo &= todo - 1) {
+      const int first = v0 + warp * 32 + __ffs(todo) - 1;
+      for (int i = first + lane * kThreads; i < v1; i += 32 * kThreads) {
+        float v[Vec<T>::N];
+        Vec<T>::values(__ldg(reinterpret_cast<const uint4*>(r.p + r.head) + i), v);
+#pragma unroll
+        for (int j = 0; j < Vec<T>::N; ++j) put_forward(v[j], (uint32_t)(r.head + i * Vec<T>::N + j));
+      }
+    }
+    if (singles && (int)threadIdx.x < r.singles()) {
+      const int at = r.single_at(threadIdx.x);
+      put_forward(load1(r.p + at), (uint32_t)at);
+    }
     __syncthreads();
     const int n = sh.n_cand;
     if (n <= kCand) {
@@ -222,7 +266,7 @@ struct FwdParams {
 
 // A row is taken by a cluster of blocks (one block when there are enough rows).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logp_fwd_kernel(const __grid_constant__ FwdParams p, int parts) {
+__global__ void __launch_bounds__(kThreads, 4) logp_fwd_kernel(const __grid_constant__ FwdParams p, int parts) {
   __shared__ LogpShared sh;
   const int64_t row = blockIdx.x / parts;
   const int part = (int)(blockIdx.x - row * parts);
@@ -235,35 +279,53 @@ __global__ void __launch_bounds__(kThreads) logp_fwd_kernel(const __grid_constan
 
   Sums a{-INFINITY, 0.f, 0.f};
   const uint4* body = reinterpret_cast<const uint4*>(r.p + r.head);
+  const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;          // -inf
+  float2 s2[2] = {both(0.f), both(0.f)}, w2[2] = {both(0.f), both(0.f)};     // the sums, in four parts
+  float2 base2 = both(0.f);                                                  // minus the maximum
+  typename Vec<T>::Floor low = Vec<T>::floor_of(-150.f / c);
+  uint4 next[U];
+  auto fetch = [&](int i) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      next[u] = i + u * kThreads < v1 ? ld_stream16(body + i + u * kThreads) : make_uint4(none, none, none, none);
+  };
+  fetch(v0 + (int)threadIdx.x);
   for (int i = v0 + (int)threadIdx.x; i < v1; i += U * kThreads) {
     uint4 raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * kThreads < v1) raw[u] = __ldg(body + i + u * kThreads);
+    for (int u = 0; u < U; ++u) raw[u] = next[u];
+    if (i + U * kThreads < v1) fetch(i + U * kThreads);
+    const float m = Vec<T>::largest(Vec<T>::larger(Vec<T>::larger(raw[0], raw[1]), Vec<T>::larger(raw[2], raw[3])));
+    if (!(m <= a.m)) {                         // grown (or NaN): bring the sums to the new maximum
+      const float nm = max_nan(m, a.m);
+      const float d = fmaxf((a.m - nm) * c, -150.f), f = exp2_fast(d);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        w2[q] = mul2(both(f), fma2(s2[q], both(d), w2[q]));
+        s2[q] = mul2(both(f), s2[q]);
+      }
+      a.m = nm;
+      base2 = both(-nm);
+      // 2^-7 |m| further down, so that rounding to T never lifts it to the maximum
+      low = Vec<T>::floor_of(fmaxf(nm - fmaf(fabsf(nm), 0.0078125f, 150.f / c), Vec<T>::kLowest));
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i + u * kThreads >= v1) break;
       float v[N];
-      Vec<T>::values(raw[u], v);
-      float m = v[0];
+      Vec<T>::values(Vec<T>::hold(raw[u], low), v);
 #pragma unroll
-      for (int j = 1; j < N; ++j) m = max_nan(m, v[j]);
-      if (!(m <= a.m)) {                       // grown (or NaN): bring the sums to the new maximum
-        const float nm = max_nan(m, a.m);
-        const float d = fmaxf((a.m - nm) * c, -150.f), f = exp2_fast(d);
-        a.w = f * (a.w + a.s * d);
-        a.s *= f;
-        a.m = nm;
-      }
-      const float base = a.m == -INFINITY ? 0.f : a.m;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float d = max_nan((v[j] - base) * c, -150.f), e = exp2_fast(d);
-        a.s += e;
-        a.w = fmaf(e, d, a.w);
+      for (int j = 0; j < N; j += 2) {
+        const float2 d = mul2(add2(make_float2(v[j], v[j + 1]), base2), both(c));
+        const float2 e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+        s2[(j >> 1) & 1] = add2(s2[(j >> 1) & 1], e);
+        w2[(j >> 1) & 1] = fma2(e, d, w2[(j >> 1) & 1]);
       }
     }
   }
+  const float2 st = add2(s2[0], s2[1]), wt = add2(w2[0], w2[1]);
+  a.s = st.x + st.y;
+  a.w = wt.x + wt.y;
+  if (a.m == -INFINITY) a.s = a.w = 0.f;       // nothing but masked entries so far
   if (part == 0 && (int)threadIdx.x < r.singles()) add_one(a, load1(r.p + r.single_at(threadIdx.x)), c);
   const float own_max = a.m;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
