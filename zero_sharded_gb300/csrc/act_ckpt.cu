@@ -1,7 +1,7 @@
 // Writing and reading 8-bit activation checkpoints (format: act_ckpt.cuh).
 //
 // Both directions are one pass over memory: s + 33/32 bytes an element (s = 2 for bf16,
-// 4 for fp32).  Rows on 16-byte boundaries take 8 elements a thread, a block of 32 being
+// 4 for fp32).  Rows on 16-byte boundaries take 8 elements at a time (16 when reading), a block of 32 being
 // 4 lanes; other strides take one element a lane, a block being a warp (one warp-wide
 // integer maximum), so that loads stay coalesced at any alignment.
 
@@ -19,46 +19,58 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 
-// Chunk i of 8 elements: row and first column.
-__device__ __forceinline__ void chunk_at(int64_t i, uint32_t per_row, int64_t& row, int& col) {
-  if (i < (int64_t)0xFFFFFFFF) {
-    const uint32_t r = (uint32_t)i / per_row;
-    row = r;
-    col = (int)((uint32_t)i - r * per_row) * 8;
-  } else {
-    row = i / per_row;
-    col = (int)(i - row * per_row) * 8;
+// Where a thread is: item i of a matrix with per_row items a row.  One division at the start; the next item, kThreads
+// further, is `rows` rows and `items` items on.
+struct Step {
+  uint32_t rows, items;
+};
+struct At {
+  int64_t row;
+  uint32_t item;
+  __device__ __forceinline__ At(int64_t i, uint32_t per_row) {
+    if (i < (int64_t)0xFFFFFFFF) {
+      const uint32_t r = (uint32_t)i / per_row;
+      row = r;
+      item = (uint32_t)i - r * per_row;
+    } else {
+      row = i / per_row;
+      item = (uint32_t)(i - row * per_row);
+    }
   }
-}
+  __device__ __forceinline__ void next(const Step& s, uint32_t per_row) {
+    row += s.rows;
+    item += s.items;
+    if (item >= per_row) {
+      item -= per_row;
+      ++row;
+    }
+  }
+};
 
+// 8 elements an item.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) encode8_kernel(const T* __restrict__ x, int64_t ld, int64_t n_chunks,
-                                                           int cols, uint8_t* __restrict__ ck, ActLayout l) {
+__global__ void __launch_bounds__(kThreads) encode8_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, uint32_t cols,
+                                                           uint8_t* __restrict__ ck, ActLayout l, Step step) {
   const uint32_t per_row = (uint32_t)(l.ld_q / 8);
-  const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+  const At first((int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x, per_row);
   Raw8<T> raw[kUnroll];
-  int64_t row[kUnroll];
-  int col[kUnroll];
+  At at = first;
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = i0 + u * kThreads;
     zero8(raw[u]);
-    row[u] = -1;
-    if (i < n_chunks) {
-      chunk_at(i, per_row, row[u], col[u]);
-      if (col[u] < cols) load8(x + row[u] * ld + col[u], raw[u]);   // cols % 8 == 0 here
-    }
+    if (at.row < rows && at.item * 8 < cols) load8(x + at.row * ld + at.item * 8, raw[u]);   // cols % 8 == 0 here
+    at.next(step, per_row);
   }
+  at = first;
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    float v[8];
-    values8(raw[u], v);
-    uint2 q;
-    const uint32_t b = act_encode8(v, &q);
-    if (row[u] >= 0) {
-      *reinterpret_cast<uint2*>(ck + row[u] * l.ld_q + col[u]) = q;
-      if ((threadIdx.x & 3) == 0) ck[l.e_off + row[u] * l.ld_e + col[u] / kActBlock] = (uint8_t)b;
+    const uint32_t b = act_block_scale(act_amax8(raw[u]));
+    const uint2 q = act_pack8(values(raw[u]), b);
+    if (at.row < rows) {
+      *reinterpret_cast<uint2*>(ck + at.row * l.ld_q + at.item * 8) = q;
+      if ((threadIdx.x & 3) == 0) ck[l.e_off + at.row * l.ld_e + at.item / 4] = (uint8_t)b;
     }
+    at.next(step, per_row);
   }
 }
 
@@ -88,31 +100,34 @@ __global__ void __launch_bounds__(kThreads) encode1_kernel(const T* __restrict__
   }
 }
 
+// 16 elements an item (the last one of a row may have 8).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) decode8_kernel(const uint8_t* __restrict__ ck, ActLayout l,
-                                                           int64_t n_chunks, int cols, T* __restrict__ x, int64_t ld) {
-  const uint32_t per_row = (uint32_t)(cols / 8);
-  const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
-  uint2 q[kUnroll];
+__global__ void __launch_bounds__(kThreads) decode16_kernel(const uint8_t* __restrict__ ck, ActLayout l, int64_t rows, uint32_t cols,
+                                                            T* __restrict__ x, int64_t ld, Step step) {
+  const uint32_t per_row = (cols + 15) / 16;
+  const At first((int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x, per_row);
+  uint4 q[kUnroll];
   uint32_t b[kUnroll];
-  int64_t row[kUnroll];
-  int col[kUnroll];
+  At at = first;
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = i0 + u * kThreads;
-    row[u] = -1;
-    if (i < n_chunks) {
-      chunk_at(i, per_row, row[u], col[u]);
-      q[u] = __ldcs(reinterpret_cast<const uint2*>(ck + row[u] * l.ld_q + col[u]));
-      b[u] = ck[l.e_off + row[u] * l.ld_e + col[u] / kActBlock];
+    if (at.row < rows) {
+      q[u] = ld_stream16(ck + at.row * l.ld_q + at.item * 16);
+      b[u] = ck[l.e_off + at.row * l.ld_e + at.item / 2];
     }
+    at.next(step, per_row);
   }
+  at = first;
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    if (row[u] < 0) continue;
-    float v[8];
-    act_decode8(q[u], b[u], v);
-    store8(x + row[u] * ld + col[u], v);
+    if (at.row < rows) {
+      const float s = act_scale(b[u]);
+      T* to = x + at.row * ld + at.item * 16;
+      const F8 lo = act_values8(make_uint2(q[u].x, q[u].y), s);
+      if (at.item * 16 + 8 < cols) store16(to, lo, act_values8(make_uint2(q[u].z, q[u].w), s));
+      else store8(to, lo);
+    }
+    at.next(step, per_row);
   }
 }
 
@@ -139,13 +154,16 @@ unsigned blocks_for(int64_t n, int64_t per_block) {
   return b > INT32_MAX ? 0u : (unsigned)b;
 }
 
+Step step_of(int64_t per_row) { return Step{(uint32_t)(kThreads / per_row), (uint32_t)(kThreads % per_row)}; }
+
 template <typename T>
 int encode(const T* x, int64_t ld, int64_t rows, int64_t cols, uint8_t* ck, cudaStream_t s) {
   const ActLayout l = act_layout(rows, cols);
   if (cols % 8 == 0 && rows_aligned(x, ld, sizeof(T))) {
-    const int64_t n = rows * (l.ld_q / 8);
-    const unsigned g = blocks_for(n, kThreads * kUnroll);
-    return g ? launch_kernel(encode8_kernel<T>, g, kThreads, 0, s, 1, x, ld, n, (int)cols, ck, l) : CZ_ERR_UNSUPPORTED;
+    const int64_t per_row = l.ld_q / 8;
+    const unsigned g = blocks_for(rows * per_row, kThreads * kUnroll);
+    return g ? launch_kernel(encode8_kernel<T>, g, kThreads, 0, s, 1, x, ld, rows, (uint32_t)cols, ck, l, step_of(per_row))
+             : CZ_ERR_UNSUPPORTED;
   }
   const int64_t n = rows * (l.ld_q / kActBlock);
   const unsigned g = blocks_for(n, kThreads / 32 * kUnroll);
@@ -156,9 +174,10 @@ template <typename T>
 int decode(const uint8_t* ck, int64_t rows, int64_t cols, T* x, int64_t ld, cudaStream_t s) {
   const ActLayout l = act_layout(rows, cols);
   if (cols % 8 == 0 && rows_aligned(x, ld, sizeof(T))) {
-    const int64_t n = rows * (cols / 8);
-    const unsigned g = blocks_for(n, kThreads * kUnroll);
-    return g ? launch_kernel(decode8_kernel<T>, g, kThreads, 0, s, 1, ck, l, n, (int)cols, x, ld) : CZ_ERR_UNSUPPORTED;
+    const int64_t per_row = div_up(cols, 16);
+    const unsigned g = blocks_for(rows * per_row, kThreads * kUnroll);
+    return g ? launch_kernel(decode16_kernel<T>, g, kThreads, 0, s, 1, ck, l, rows, (uint32_t)cols, x, ld, step_of(per_row))
+             : CZ_ERR_UNSUPPORTED;
   }
   const int64_t n = rows * (l.ld_q / kActBlock);
   const unsigned g = blocks_for(n, kThreads / 32 * kUnroll);
@@ -179,6 +198,28 @@ int check_sm103() {
   known = (major == 10 && minor == 3) ? CZ_OK : CZ_ERR_UNSUPPORTED;
   known_dev = dev;
   return known;
+}
+
+int blocks_per_sm(const void* kernel, int threads, int smem) {
+  struct Known {
+    const void* kernel;
+    int dev, threads, smem, blocks;
+  };
+  static thread_local Known known[64] = {};
+  int dev = 0;
+  if (note_cuda_error(cudaGetDevice(&dev)) != cudaSuccess) return 0;
+  Known& k = known[((reinterpret_cast<uintptr_t>(kernel) >> 4) * 31 + (uintptr_t)threads * 7 + (uintptr_t)smem / 16) % 64];
+  if (k.kernel == kernel && k.dev == dev && k.threads == threads && k.smem == smem) return k.blocks;
+  // the attribute stays at the largest size asked for: a smaller launch may follow a larger one's entry
+  cudaFuncAttributes a;
+  if (note_cuda_error(cudaFuncGetAttributes(&a, kernel)) != cudaSuccess) return 0;
+  if (smem > a.maxDynamicSharedSizeBytes &&
+      note_cuda_error(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+    return 0;
+  int n = 0;
+  if (note_cuda_error(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, (size_t)smem)) != cudaSuccess) return 0;
+  k = Known{kernel, dev, threads, smem, n};
+  return n;
 }
 
 int sm_count() {

@@ -73,24 +73,55 @@ __device__ __forceinline__ uint32_t act_quantise(float x, float inv, uint32_t b)
 // |x| as ordered bits.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// 8 consecutive elements of a row, the 4 lanes of an aligned group of 4 holding one
-// block: the group's scale byte, and the 8 q packed.  Every lane of the warp calls.
-__device__ __forceinline__ uint32_t act_encode8(const float* v, uint2* q) {
-  uint32_t m = 0;
+// The 8 q of v packed.  The product is exact and the sum rounds it, so one fused operation does both.
+__device__ __forceinline__ uint2 act_pack8(const F8& v, uint32_t b) {
+  uint32_t r[8];
+  if (b < 249u) {
+    const float2 inv = both(act_inv_scale(b)), magic = both(12582912.f);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const uint32_t b = act_scale_byte(m);
-  const float inv = act_inv_scale(b);
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = fma2(v.p[i], inv, magic);
+      r[2 * i] = __float_as_uint(t.x);
+      r[2 * i + 1] = __float_as_uint(t.y);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = act_quantise(v.get(j), act_inv_scale(b), b);
+  }
   uint32_t w[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t q0 = act_quantise(v[4 * h], inv, b), q1 = act_quantise(v[4 * h + 1], inv, b);
-    const uint32_t q2 = act_quantise(v[4 * h + 2], inv, b), q3 = act_quantise(v[4 * h + 3], inv, b);
-    w[h] = q0 | (q1 << 8) | (q2 << 16) | (q3 << 24);
-  }
-  *q = make_uint2(w[0], w[1]);
+  for (int h = 0; h < 2; ++h)
+    w[h] = __byte_perm(__byte_perm(r[4 * h], r[4 * h + 1], 0x0040), __byte_perm(r[4 * h + 2], r[4 * h + 3], 0x0040), 0x5410);
+  return make_uint2(w[0], w[1]);
+}
+
+// Bits of the largest |x| of 8 (NaN above everything).
+__device__ __forceinline__ float max_nan_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+__device__ __forceinline__ uint32_t act_amax8(const F8& v) {
+  const float a = max_nan_abs(max_nan_abs(v.p[0].x, v.p[0].y), max_nan_abs(v.p[1].x, v.p[1].y));
+  const float b = max_nan_abs(max_nan_abs(v.p[2].x, v.p[2].y), max_nan_abs(v.p[3].x, v.p[3].y));
+  return abs_bits(max_nan_abs(a, b));
+}
+__device__ __forceinline__ uint32_t act_amax8(const Raw8<float>& r) { return act_amax8(values(r)); }
+__device__ __forceinline__ uint32_t act_amax8(const Raw8<__nv_bfloat16>& r) {
+  const uint32_t m = 0x7FFF7FFFu;
+  const uint32_t a = __vmaxu2(__vmaxu2(r.a.x & m, r.a.y & m), __vmaxu2(r.a.z & m, r.a.w & m));
+  return max(a << 16, a & 0xFFFF0000u);
+}
+
+// 8 consecutive elements of a row, the 4 lanes of an aligned group of 4 holding one
+// block: the group's scale byte, from the largest |x| of the lane's 8.  Every lane of the warp calls.
+__device__ __forceinline__ uint32_t act_block_scale(uint32_t amax_bits) {
+  amax_bits = max(amax_bits, __shfl_xor_sync(0xffffffffu, amax_bits, 1));
+  return act_scale_byte(max(amax_bits, __shfl_xor_sync(0xffffffffu, amax_bits, 2)));
+}
+__device__ __forceinline__ uint32_t act_encode8(const F8& v, uint2* q) {
+  const uint32_t b = act_block_scale(act_amax8(v));
+  *q = act_pack8(v, b);
   return b;
 }
 
@@ -103,15 +134,7 @@ __device__ __forceinline__ uint32_t act_encode1(float v, uint32_t* q) {
 
 // q + 128 as the low mantissa byte of 2^23: one difference gives q, one product x^ (both exact; integer
 // conversions run at an eighth of the rate).
-__device__ __forceinline__ void act_decode8(uint2 q, uint32_t b, float* v) {
-  const float s = act_scale(b);
-  const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    v[j] = (__uint_as_float(__byte_perm(w[j >> 2], 0x4B000000u, 0x7540u | (uint32_t)(j & 3))) - 8388736.f) * s;
-}
-
-// The 8 values of w (q), scaled by s: s = 2^E, or 2^E times a factor to round once.
+// s: 2^E, or 2^E times a factor, by which each value is then rounded once.
 __device__ __forceinline__ F8 act_values8(uint2 q, float s) {
   const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
   F8 v;

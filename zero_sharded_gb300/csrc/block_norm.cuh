@@ -56,7 +56,7 @@ __device__ __forceinline__ void gate_value_slope(float g, int act, float& value,
   }
 }
 
-// 8 elements of a chunk from a matrix row (VEC) or from strided columns.
+// 8 elements of a chunk from a matrix row, zero past its end (VEC: as raw registers, the loads in flight).
 template <typename T, bool VEC>
 struct Chunk;
 template <typename T>
@@ -66,26 +66,29 @@ struct Chunk<T, true> {
     const int col = col_of<true>(c, 0, t, n);
     if (col < cols) load8(row + col, r); else zero8(r);
   }
-  __device__ __forceinline__ void values(float* v) const { values8(r, v); }
+  __device__ __forceinline__ F8 get() const { return values(r); }
 };
 template <typename T>
 struct Chunk<T, false> {
-  float v8[8];
+  T r[8];
   __device__ __forceinline__ void load(const T* row, int c, int t, int n, int cols) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int col = col_of<false>(c, j, t, n);
-      v8[j] = col < cols ? load1(row + col) : 0.f;
+      r[j] = T(0.f);
+      if (col < cols) r[j] = row[col];
     }
   }
-  __device__ __forceinline__ void values(float* v) const {
+  __device__ __forceinline__ F8 get() const {
+    F8 v;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v8[j];
+    for (int j = 0; j < 8; ++j) v.set(j, (float)r[j]);
+    return v;
   }
 };
 
 template <bool VEC, typename T>
-__device__ __forceinline__ void store_chunk(T* row, const float* v, int c, int t, int n, int cols) {
+__device__ __forceinline__ void put(T* row, const F8& v, int c, int t, int n, int cols) {
   if constexpr (VEC) {
     const int col = col_of<true>(c, 0, t, n);
     if (col < cols) store8(row + col, v);
@@ -93,35 +96,7 @@ __device__ __forceinline__ void store_chunk(T* row, const float* v, int c, int t
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int col = col_of<false>(c, j, t, n);
-      if (col < cols) store1(row + col, v[j]);
-    }
-  }
-}
-
-// 8 elements of a vector over the columns (fp32, any alignment): stays in the first-level
-// cache, every row of the block reads it again.
-template <bool VEC>
-__device__ __forceinline__ void load_vector(const float* w, bool vec16, float* v, int c, int t, int n, int cols) {
-  if constexpr (VEC) {
-    const int col = col_of<true>(c, 0, t, n);
-    if (col < cols) {
-      if (vec16) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(w + col)), b = __ldg(reinterpret_cast<const float4*>(w + col) + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __ldg(w + col + j);
-      }
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<false>(c, j, t, n);
-      v[j] = col < cols ? __ldg(w + col) : 0.f;
+      if (col < cols) store1(row + col, v.get(j));
     }
   }
 }
@@ -129,7 +104,7 @@ __device__ __forceinline__ void load_vector(const float* w, bool vec16, float* v
 // Writes the chunk's part of a checkpoint row; every lane of the warp calls, `live` says
 // whether the row exists.
 template <bool VEC>
-__device__ __forceinline__ void keep_chunk(uint8_t* ck, const ActLayout& l, int64_t row, bool live, const float* v, int c,
+__device__ __forceinline__ void keep_chunk(uint8_t* ck, const ActLayout& l, int64_t row, bool live, const F8& v, int c,
                                            int t, int n) {
   if constexpr (VEC) {
     uint2 q;
@@ -143,7 +118,7 @@ __device__ __forceinline__ void keep_chunk(uint8_t* ck, const ActLayout& l, int6
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       uint32_t q;
-      const uint32_t b = act_encode1(v[j], &q);
+      const uint32_t b = act_encode1(v.get(j), &q);
       const int col = col_of<false>(c, j, t, n);
       if (live && col < l.ld_q) {
         ck[row * l.ld_q + col] = (uint8_t)q;
@@ -155,5 +130,11 @@ __device__ __forceinline__ void keep_chunk(uint8_t* ck, const ActLayout& l, int6
 
 __device__ __forceinline__ int round8(int v) { return (v + 7) & ~7; }
 __device__ __forceinline__ int round4(int v) { return (v + 3) & ~3; }
+
+// Where column `col` of a vector lies in shared memory: the first and second four of every 8 columns in halves of their
+// own, so that lanes 8 columns apart read 16 bytes next to one another.
+__device__ __forceinline__ int plane_at(int col, int cols) {
+  return (col & 4 ? round8(cols) >> 1 : 0) + ((col >> 3) << 2) + (col & 3);
+}
 
 }  // namespace cz

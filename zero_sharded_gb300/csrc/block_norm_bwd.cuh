@@ -128,12 +128,6 @@ __device__ __forceinline__ F8 take_kept(const uint8_t* q, const uint8_t* e, cons
   return v;
 }
 
-// Where column `col` of a vector lies in shared memory: the first and second four of every 8 columns in halves of their
-// own, so that lanes 8 columns apart read 16 bytes next to one another.
-__device__ __forceinline__ int plane_at(int col, int cols) {
-  return (col & 4 ? round8(cols) >> 1 : 0) + ((col >> 3) << 2) + (col & 3);
-}
-
 // 8 elements of a vector over the columns, in shared memory (RING) or memory.
 template <bool VEC, bool RING>
 __device__ __forceinline__ F8 take_vector(const float* w, int c, int t, int n, int cols) {
@@ -160,20 +154,6 @@ __device__ __forceinline__ F8 take_vector(const float* w, int c, int t, int n, i
     }
   }
   return v;
-}
-
-template <bool VEC, typename T>
-__device__ __forceinline__ void put(T* row, const F8& v, int c, int t, int n, int cols) {
-  if constexpr (VEC) {
-    const int col = col_of<true>(c, 0, t, n);
-    if (col < cols) store8(row + col, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<false>(c, j, t, n);
-      if (col < cols) store1(row + col, v.get(j));
-    }
-  }
 }
 
 // Barrier of the n threads of row group g.
@@ -505,7 +485,12 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
     if constexpr (!SOLO) {
       __syncthreads();
 #pragma unroll
-      for (int c = 0; c < C; ++c) put<VEC>(fold + g * round4(cols), v == 0 ? a_post[c] : v == 1 ? a_pre[c] : a_gate[c], c, t, n, cols);
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int col = col_of<VEC>(c, j, t, n);
+          if (col < cols) fold[g * round4(cols) + col] = (v == 0 ? a_post[c] : v == 1 ? a_pre[c] : a_gate[c]).get(j);
+        }
       __syncthreads();
       for (int col = threadIdx.x; col < cols; col += blockDim.x) {
         float s = 0.f;
@@ -567,8 +552,7 @@ int launch_ring(const NormParams& p, const BwdLayout& l, int blocks, cudaStream_
             : p.row_threads > 256 && p.row_threads <= 640 ? norm_bwd_kernel<TH, TY, VEC, 1, 640, true, true, CHANNEL, MODE>
             : p.row_threads <= 256 ? norm_bwd_kernel<TH, TY, VEC, 1, 256, true, true, CHANNEL, MODE>
                                    : norm_bwd_kernel<TH, TY, VEC, 1, 1024, true, true, CHANNEL, MODE>;
-  if (note_cuda_error(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-    return CZ_ERR_CUDA;
+  if (blocks_per_sm(reinterpret_cast<const void*>(k), p.row_threads * p.rows_per_block, (int)smem) < 1) return CZ_ERR_CUDA;
   return launch_kernel(k, dim3((unsigned)blocks), dim3((unsigned)(p.row_threads * p.rows_per_block)), (size_t)smem, s, 1, p, l);
 }
 

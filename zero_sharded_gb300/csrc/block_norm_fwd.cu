@@ -6,7 +6,9 @@
 // rounded once, when they are stored, and r_h is that of the unrounded h'.
 //
 // One pass: a row lives in the registers of its threads from its load to its stores.
-// Bound by memory: 2 s_h + 2 s_y bytes an element, 33/32 more for every checkpoint.
+// Bound by memory: 2 s_h + 2 s_y bytes an element, 33/32 more for every checkpoint.  Blocks walk over rows: the
+// next row's loads are in flight while this one is joined, scaled and stored, and the vectors over the columns
+// stay in shared memory.
 
 #include <cuda_runtime.h>
 
@@ -16,99 +18,166 @@
 namespace cz {
 namespace {
 
+// A vector over the columns in shared memory (aligned rows: two planes), or ones.
+struct FwdVectors {
+  int32_t post, pre, gate, floats;   // offsets in floats; < 0: not there
+};
+
+template <bool VEC>
+__device__ __forceinline__ F8 shared_vector(const float* w, int c, int t, int n, int cols) {
+  F8 v;
+  if constexpr (VEC) {
+    const int col = col_of<true>(c, 0, t, n);
+    const float4 a = *reinterpret_cast<const float4*>(w + (col >> 1));
+    const float4 b = *reinterpret_cast<const float4*>(w + (col >> 1) + (round8(cols) >> 1));
+    v.p[0] = make_float2(a.x, a.y);
+    v.p[1] = make_float2(a.z, a.w);
+    v.p[2] = make_float2(b.x, b.y);
+    v.p[3] = make_float2(b.z, b.w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = col_of<false>(c, j, t, n);
+      v.set(j, col < cols ? w[col] : 0.f);
+    }
+  }
+  return v;
+}
+
 template <typename TH, typename TY, bool VEC, int C, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(MAXT, 1) norm_fwd_kernel(const __grid_constant__ NormParams p, const FwdVectors at) {
   __shared__ float red[2][32];
+  extern __shared__ __align__(16) float vec[];
   const int n = p.row_threads, g = threadIdx.x / n, t = threadIdx.x - g * n, row_warps = n >> 5;
-  const int64_t row = (int64_t)blockIdx.x * p.rows_per_block + g;
-  const bool live = row < p.rows;
-  const int cols = live ? p.cols : 0;
-  const int64_t r = live ? row : 0;
-  const TH* h = static_cast<const TH*>(p.h) + r * p.ld_h;
-  const TY* y = static_cast<const TY*>(p.y) + r * p.ld_y;
-  const TY* gate = static_cast<const TY*>(p.gate) + r * p.ld_gate;
+  const int cols = p.cols;
+  const float inv_n = 1.f / (float)cols;
+  for (int i = threadIdx.x; i < cols; i += blockDim.x) {
+    const int to = VEC ? plane_at(i, cols) : i;
+    if (at.post >= 0) vec[at.post + to] = p.w_post[i];
+    if (at.pre >= 0) vec[at.pre + to] = p.w_pre[i];
+    if (at.gate >= 0) vec[at.gate + to] = gate_value(static_cast<const float*>(p.gate)[i], p.gate_act);
+  }
+  __syncthreads();
+  bool in[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) in[c] = !VEC || col_of<VEC>(c, 0, t, n) < cols;
+  const bool token = p.gate_kind == kGateToken;
+
   Chunk<TY, VEC> ry[C], rg[C];
   Chunk<TH, VEC> rh[C];
+  auto fetch = [&](int64_t row) {
+    const int in_row = row < p.rows ? cols : 0;
+    const int64_t r = row < p.rows ? row : 0;
 #pragma unroll
-  for (int c = 0; c < C; ++c) ry[c].load(y, c, t, n, cols);
-#pragma unroll
-  for (int c = 0; c < C; ++c) rh[c].load(h, c, t, n, cols);
-  if (p.gate_kind == kGateToken) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) rg[c].load(gate, c, t, n, cols);
-  }
-  float r_post = 1.f;
-  if (p.post) {
+    for (int c = 0; c < C; ++c) {
+      ry[c].load(static_cast<const TY*>(p.y) + r * p.ld_y, c, t, n, in_row);
+      rh[c].load(static_cast<const TH*>(p.h) + r * p.ld_h, c, t, n, in_row);
+      if (token) rg[c].load(static_cast<const TY*>(p.gate) + r * p.ld_gate, c, t, n, in_row);
+    }
+  };
+  const int64_t stride = (int64_t)gridDim.x * p.rows_per_block;
+  fetch((int64_t)blockIdx.x * p.rows_per_block + g);
+  for (int64_t base = (int64_t)blockIdx.x * p.rows_per_block; base < p.rows; base += stride) {
+    const int64_t row = base + g;
+    const bool live = row < p.rows;
+    const int64_t r = live ? row : 0;
+    const int in_row = live ? cols : 0;
+    F8 v[C], h[C];
     float s = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float v[8];
-      ry[c].values(v);
+      v[c] = ry[c].get();
+      float2 part = mul2(v[c].p[0], v[c].p[0]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
+      for (int j = 1; j < 4; ++j) part = fma2(v[c].p[j], v[c].p[j], part);
+      s += part.x + part.y;
+      if (p.y_ckpt) keep_chunk<VEC>(p.y_ckpt, p.ck, row, live, v[c], c, t, n);
     }
-    r_post = 1.f / sqrtf(row_sum(s, red[0], row_warps) / (float)p.cols + p.eps);
-    if (p.rstd_post && live && t == 0) p.rstd_post[row] = r_post;
-  }
-  const bool wp16 = (reinterpret_cast<uintptr_t>(p.w_post) & 15) == 0, wx16 = (reinterpret_cast<uintptr_t>(p.w_pre) & 15) == 0,
-             g16 = (reinterpret_cast<uintptr_t>(p.gate) & 15) == 0;
-  float hv[C][8];
-  float s = 0.f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    float v[8], w[8];
-    ry[c].values(v);
-    if (p.y_ckpt) keep_chunk<VEC>(p.y_ckpt, p.ck, row, live, v, c, t, n);
+    float r_post = 1.f;
     if (p.post) {
+      r_post = 1.f / sqrtf(fmaf(row_sum(s, red[0], row_warps), inv_n, p.eps));
+      if (p.rstd_post && live && t == 0) p.rstd_post[row] = r_post;
+    }
+    s = 0.f;
+    const float k = p.y_scale * r_post;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= r_post;
-      if (p.w_post) {
-        load_vector<VEC>(p.w_post, wp16, w, c, t, n, cols);
+    for (int c = 0; c < C; ++c) {
+      h[c] = rh[c].get();
+      if (in[c]) {
+        if (at.post >= 0) {
+          const F8 w = shared_vector<VEC>(vec + at.post, c, t, n, cols);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= w[j];
+          for (int j = 0; j < 4; ++j) v[c].p[j] = mul2(v[c].p[j], w.p[j]);
+        }
+        if (p.gate_kind != kGateNone) {
+          F8 w;
+          if (token) {
+            w = rg[c].get();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w.set(j, gate_value(w.get(j), p.gate_act));
+          } else {
+            w = shared_vector<VEC>(vec + at.gate, c, t, n, cols);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[c].p[j] = mul2(v[c].p[j], w.p[j]);
+        }
       }
+      float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[c].p[j] = fma2(both(k), v[c].p[j], mul2(both(p.h_scale), h[c].p[j]));
+        part = fma2(h[c].p[j], h[c].p[j], part);
+      }
+      s += part.x + part.y;
     }
-    if (p.gate_kind != kGateNone) {
-      if (p.gate_kind == kGateChannel) load_vector<VEC>(static_cast<const float*>(p.gate), g16, w, c, t, n, cols);
-      else rg[c].values(w);
+    fetch(base + stride + g);                  // in flight until the next turn
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= gate_value(w[j], p.gate_act);
+    for (int c = 0; c < C; ++c) {
+      if (p.h_out) put<VEC>(static_cast<TH*>(p.h_out) + r * p.ld_h_out, h[c], c, t, n, in_row);
+      if (p.h_ckpt) keep_chunk<VEC>(p.h_ckpt, p.ck, row, live, h[c], c, t, n);
     }
-    rh[c].values(hv[c]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      hv[c][j] = fmaf(p.y_scale, v[j], p.h_scale * hv[c][j]);
-      s = fmaf(hv[c][j], hv[c][j], s);
+    if (!p.pre) {
+      if (p.post && row_warps > 1) __syncthreads();   // red[0] is read before the next row writes it
+      continue;
     }
-    if (p.h_out) store_chunk<VEC>(static_cast<TH*>(p.h_out) + r * p.ld_h_out, hv[c], c, t, n, cols);
-    if (p.h_ckpt) keep_chunk<VEC>(p.h_ckpt, p.ck, row, live, hv[c], c, t, n);
-  }
-  if (!p.pre) return;
-  const float r_pre = 1.f / sqrtf(row_sum(s, red[1], row_warps) / (float)p.cols + p.eps);
-  if (p.rstd_pre && live && t == 0) p.rstd_pre[row] = r_pre;
+    const float r_pre = 1.f / sqrtf(fmaf(row_sum(s, red[1], row_warps), inv_n, p.eps));
+    if (p.rstd_pre && live && t == 0) p.rstd_pre[row] = r_pre;
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    float w[8];
+    for (int c = 0; c < C; ++c) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) hv[c][j] *= r_pre;
-    if (p.w_pre) {
-      load_vector<VEC>(p.w_pre, wx16, w, c, t, n, cols);
+      for (int j = 0; j < 4; ++j) h[c].p[j] = mul2(h[c].p[j], both(r_pre));
+      if (at.pre >= 0 && in[c]) {
+        const F8 w = shared_vector<VEC>(vec + at.pre, c, t, n, cols);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) hv[c][j] *= w[j];
+        for (int j = 0; j < 4; ++j) h[c].p[j] = mul2(h[c].p[j], w.p[j]);
+      }
+      if (p.x) put<VEC>(static_cast<TY*>(p.x) + r * p.ld_x, h[c], c, t, n, in_row);
+      if (p.x_ckpt) keep_chunk<VEC>(p.x_ckpt, p.ck, row, live, h[c], c, t, n);
     }
-    if (p.x) store_chunk<VEC>(static_cast<TY*>(p.x) + r * p.ld_x, hv[c], c, t, n, cols);
-    if (p.x_ckpt) keep_chunk<VEC>(p.x_ckpt, p.ck, row, live, hv[c], c, t, n);
+    if (!p.post && row_warps > 1) __syncthreads();    // likewise red[1]
   }
 }
 
 template <typename TH, typename TY, bool VEC>
 int launch_c(const NormParams& p, cudaStream_t s) {
-  const int64_t blocks = div_up(p.rows, p.rows_per_block);
-  if (blocks > INT32_MAX) return CZ_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks), block((unsigned)(p.row_threads * p.rows_per_block));
-  if (p.row_threads * 8 >= p.cols) return launch_kernel(norm_fwd_kernel<TH, TY, VEC, 1, 512>, grid, block, 0, s, 1, p);
-  if (p.row_threads <= 512) return launch_kernel(norm_fwd_kernel<TH, TY, VEC, 2, 512>, grid, block, 0, s, 1, p);
-  return launch_kernel(norm_fwd_kernel<TH, TY, VEC, 2, 1024>, grid, block, 0, s, 1, p);
+  const int threads = p.row_threads * p.rows_per_block;
+  FwdVectors at{-1, -1, -1, 0};
+  auto vector = [&](bool on) {
+    if (!on) return int32_t{-1};
+    at.floats += (int32_t)round_up(p.cols, 8);
+    return at.floats - (int32_t)round_up(p.cols, 8);
+  };
+  at.post = vector(p.post && p.w_post);
+  at.pre = vector(p.pre && p.w_pre);
+  at.gate = vector(p.gate_kind == kGateChannel);
+  const int smem = at.floats * 4;
+  auto* k = p.row_threads * 8 >= p.cols ? norm_fwd_kernel<TH, TY, VEC, 1, 512>
+            : p.row_threads <= 512 ? norm_fwd_kernel<TH, TY, VEC, 2, 512>
+                                   : norm_fwd_kernel<TH, TY, VEC, 2, 1024>;
+  const int per_sm = blocks_per_sm(reinterpret_cast<const void*>(k), threads, smem);
+  if (per_sm < 1) return CZ_ERR_CUDA;
+  const int64_t blocks = std::min<int64_t>(div_up(p.rows, p.rows_per_block), (int64_t)per_sm * sm_count());
+  return launch_kernel(k, dim3((unsigned)blocks), dim3((unsigned)threads), (size_t)smem, s, 1, p, at);
 }
 
 template <typename TH, typename TY>

@@ -64,4 +64,8 @@ int launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, 
                                                                                                        : CZ_ERR_CUDA;
 }
 
+// Prepares `kernel` for `smem` bytes of dynamic shared memory and says how many of its blocks an SM holds (0: it
+// cannot run).  Both are asked of the driver once for each kernel, size and device, not on every call.
+int blocks_per_sm(const void* kernel, int threads, int smem);
+
 }  // namespace cz

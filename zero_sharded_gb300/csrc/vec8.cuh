@@ -29,25 +29,31 @@ __device__ __forceinline__ uint4 ld_stream16(const void* p) {
   return r;
 }
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, Raw8<__nv_bfloat16>& r) { r.a = ld_stream16(p); }
-__device__ __forceinline__ void load8(const float* p, Raw8<float>& r) {
-  r.a = ld_stream16(p);
-  r.b = ld_stream16(p + 4);
+// Of global memory only: a whole 32-byte sector in one access where it lies on its boundary; else the second half finds the sector in the
+// first-level cache.
+__device__ __forceinline__ void ld_sector(const void* p, uint4& a, uint4& b) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
+  } else {
+    a = static_cast<const uint4*>(p)[0];
+    b = static_cast<const uint4*>(p)[1];
+  }
 }
+__device__ __forceinline__ void st_sector(void* p, const uint4& a, const uint4& b) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+                 "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = a;
+    static_cast<uint4*>(p)[1] = b;
+  }
+}
+__device__ __forceinline__ void load8(const float* p, Raw8<float>& r) { ld_sector(p, r.a, r.b); }
 __device__ __forceinline__ void zero8(Raw8<__nv_bfloat16>& r) { r.a = make_uint4(0, 0, 0, 0); }
 __device__ __forceinline__ void zero8(Raw8<float>& r) { r.a = r.b = make_uint4(0, 0, 0, 0); }
-__device__ __forceinline__ void values8(const Raw8<__nv_bfloat16>& r, float* v) { unpack8(r.a, v); }
-__device__ __forceinline__ void values8(const Raw8<float>& r, float* v) {
-  v[0] = __uint_as_float(r.a.x); v[1] = __uint_as_float(r.a.y);
-  v[2] = __uint_as_float(r.a.z); v[3] = __uint_as_float(r.a.w);
-  v[4] = __uint_as_float(r.b.x); v[5] = __uint_as_float(r.b.y);
-  v[6] = __uint_as_float(r.b.z); v[7] = __uint_as_float(r.b.w);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) { *reinterpret_cast<uint4*>(p) = pack8(v); }
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-
 // Pairs of fp32: one instruction for both halves, each rounded as the scalar operation.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -103,13 +109,20 @@ __device__ __forceinline__ F8 values(const Raw8<float>& r) {
   v.p[3] = make_float2(__uint_as_float(r.b.z), __uint_as_float(r.b.w));
   return v;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& v) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v.p[0].x, v.p[0].y), pack_bf16x2(v.p[1].x, v.p[1].y),
-                                            pack_bf16x2(v.p[2].x, v.p[2].y), pack_bf16x2(v.p[3].x, v.p[3].y));
+__device__ __forceinline__ uint4 pack(const F8& v) {
+  return make_uint4(pack_bf16x2(v.p[0].x, v.p[0].y), pack_bf16x2(v.p[1].x, v.p[1].y), pack_bf16x2(v.p[2].x, v.p[2].y),
+                    pack_bf16x2(v.p[3].x, v.p[3].y));
 }
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& v) { *reinterpret_cast<uint4*>(p) = pack(v); }
 __device__ __forceinline__ void store8(float* p, const F8& v) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v.p[0].x, v.p[0].y, v.p[1].x, v.p[1].y);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v.p[2].x, v.p[2].y, v.p[3].x, v.p[3].y);
+  auto u = [](float f) { return __float_as_uint(f); };
+  st_sector(p, make_uint4(u(v.p[0].x), u(v.p[0].y), u(v.p[1].x), u(v.p[1].y)),
+            make_uint4(u(v.p[2].x), u(v.p[2].y), u(v.p[3].x), u(v.p[3].y)));
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const F8& v, const F8& w) { st_sector(p, pack(v), pack(w)); }
+__device__ __forceinline__ void store16(float* p, const F8& v, const F8& w) {
+  store8(p, v);
+  store8(p + 8, w);
 }
 
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
