@@ -58,8 +58,8 @@ NormParams params_of(const cz_norm_args& a, bool backward) {
   p.rows = a.rows;
   p.cols = (int32_t)a.cols;
   // The backward holds eight fp32 values an element in registers: 8 elements a thread as long as a row
-  // fits 1024 threads.  The forward holds four.
-  const int64_t per = a.cols <= 8 * (backward ? 1024 : 512) ? 8 : 16;
+  // fits 1024 threads.  The forward holds four, and 16 a thread halve what a row costs every thread.
+  const int64_t per = a.cols <= 8 * (backward ? 1024 : 256) ? 8 : 16;
   p.row_threads = (int32_t)round_up(div_up(a.cols, per), 32);
   p.rows_per_block = std::max(1, 256 / p.row_threads);   // narrow rows share a block of up to 8 warps
   p.post = a.post_norm;

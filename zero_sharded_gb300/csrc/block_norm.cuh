@@ -17,21 +17,6 @@ __device__ __forceinline__ int col_of(int c, int j, int t, int n) {
   return VEC ? (c * n + t) * 8 + j : (c * 8 + j) * n + t;
 }
 
-// Sum of v over the threads of a row.  One warp a row needs no shared memory; otherwise
-// `red` holds a float for every warp of the block and the block synchronises once, so
-// consecutive sums alternate between two such arrays.
-__device__ __forceinline__ float row_sum(float v, float* red, int row_warps) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if (row_warps == 1) return v;
-  const int warp = threadIdx.x >> 5, first = warp / row_warps * row_warps;
-  if ((threadIdx.x & 31) == 0) red[warp] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < row_warps; ++i) s += red[first + i];
-  return s;
-}
-
 __device__ __forceinline__ float gate_value(float g, int act) {
   if (act == CZ_GATE_IDENTITY) return g;
   const float s = 1.f / (1.f + __expf(-g));

@@ -44,13 +44,33 @@ __device__ __forceinline__ F8 shared_vector(const float* w, int c, int t, int n,
   return v;
 }
 
-template <typename TH, typename TY, bool VEC, int C, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) norm_fwd_kernel(const __grid_constant__ NormParams p, const FwdVectors at) {
+// Sum of v over the threads of a row; `red` holds a float for every warp of the block, and consecutive sums alternate
+// between two such arrays (one barrier a sum).
+template <bool SOLO>
+__device__ __forceinline__ float row_sum(float v, float* red, int row_warps) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if (row_warps == 1) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = SOLO ? 0 : warp / row_warps * row_warps;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  v = lane < row_warps ? red[first + lane] : 0.f;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// SOLO: a row a block.  FULL: both norms with weights, h' and x wanted, of the checkpoints at most x's.
+template <typename TH, typename TY, bool VEC, int C, int MAXT, int MINB, bool SOLO, bool FULL>
+__global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const __grid_constant__ NormParams p, const FwdVectors at) {
   __shared__ float red[2][32];
   extern __shared__ __align__(16) float vec[];
-  const int n = p.row_threads, g = threadIdx.x / n, t = threadIdx.x - g * n, row_warps = n >> 5;
+  const int n = SOLO ? (int)blockDim.x : p.row_threads;
+  const int g = SOLO ? 0 : threadIdx.x / n, t = threadIdx.x - g * n, row_warps = n >> 5;
+  const int groups = SOLO ? 1 : p.rows_per_block;
   const int cols = p.cols;
   const float inv_n = 1.f / (float)cols;
+  const bool post = FULL || p.post, pre = FULL || p.pre, w_post = FULL || at.post >= 0, w_pre = FULL || at.pre >= 0;
   for (int i = threadIdx.x; i < cols; i += blockDim.x) {
     const int to = VEC ? plane_at(i, cols) : i;
     if (at.post >= 0) vec[at.post + to] = p.w_post[i];
@@ -65,22 +85,29 @@ __global__ void __launch_bounds__(MAXT, 1) norm_fwd_kernel(const __grid_constant
 
   Chunk<TY, VEC> ry[C], rg[C];
   Chunk<TH, VEC> rh[C];
-  auto fetch = [&](int64_t row) {
-    const int in_row = row < p.rows ? cols : 0;
-    const int64_t r = row < p.rows ? row : 0;
+  const int64_t stride = (int64_t)gridDim.x * groups;
+  int64_t row = (int64_t)blockIdx.x * groups + g;
+  const TY* y = static_cast<const TY*>(p.y) + row * p.ld_y;
+  const TH* h_in = static_cast<const TH*>(p.h) + row * p.ld_h;
+  const TY* gate = token ? static_cast<const TY*>(p.gate) + row * p.ld_gate : nullptr;
+  TH* h_out = static_cast<TH*>(p.h_out) + row * p.ld_h_out;
+  TY* x = static_cast<TY*>(p.x) + row * p.ld_x;
+  auto fetch = [&](bool live) {
+    const int in_row = live ? cols : 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      ry[c].load(static_cast<const TY*>(p.y) + r * p.ld_y, c, t, n, in_row);
-      rh[c].load(static_cast<const TH*>(p.h) + r * p.ld_h, c, t, n, in_row);
-      if (token) rg[c].load(static_cast<const TY*>(p.gate) + r * p.ld_gate, c, t, n, in_row);
+      ry[c].load(y, c, t, n, in_row);
+      rh[c].load(h_in, c, t, n, in_row);
+      if (token) rg[c].load(gate, c, t, n, in_row);
     }
+    y += stride * p.ld_y;
+    h_in += stride * p.ld_h;
+    if (token) gate += stride * p.ld_gate;
   };
-  const int64_t stride = (int64_t)gridDim.x * p.rows_per_block;
-  fetch((int64_t)blockIdx.x * p.rows_per_block + g);
-  for (int64_t base = (int64_t)blockIdx.x * p.rows_per_block; base < p.rows; base += stride) {
-    const int64_t row = base + g;
-    const bool live = row < p.rows;
-    const int64_t r = live ? row : 0;
+  fetch(row < p.rows);
+  for (int64_t base = (int64_t)blockIdx.x * groups; base < p.rows;
+       base += stride, row += stride, h_out += stride * p.ld_h_out, x += stride * p.ld_x) {
+    const bool live = SOLO || row < p.rows;
     const int in_row = live ? cols : 0;
     F8 v[C], h[C];
     float s = 0.f;
@@ -91,11 +118,11 @@ __global__ void __launch_bounds__(MAXT, 1) norm_fwd_kernel(const __grid_constant
 #pragma unroll
       for (int j = 1; j < 4; ++j) part = fma2(v[c].p[j], v[c].p[j], part);
       s += part.x + part.y;
-      if (p.y_ckpt) keep_chunk<VEC>(p.y_ckpt, p.ck, row, live, v[c], c, t, n);
+      if (!FULL && p.y_ckpt) keep_chunk<VEC>(p.y_ckpt, p.ck, row, live, v[c], c, t, n);
     }
     float r_post = 1.f;
-    if (p.post) {
-      r_post = 1.f / sqrtf(fmaf(row_sum(s, red[0], row_warps), inv_n, p.eps));
+    if (post) {
+      r_post = rsqrtf(fmaf(row_sum<SOLO>(s, red[0], row_warps), inv_n, p.eps));
       if (p.rstd_post && live && t == 0) p.rstd_post[row] = r_post;
     }
     s = 0.f;
@@ -104,7 +131,7 @@ __global__ void __launch_bounds__(MAXT, 1) norm_fwd_kernel(const __grid_constant
     for (int c = 0; c < C; ++c) {
       h[c] = rh[c].get();
       if (in[c]) {
-        if (at.post >= 0) {
+        if (w_post) {
           const F8 w = shared_vector<VEC>(vec + at.post, c, t, n, cols);
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[c].p[j] = mul2(v[c].p[j], w.p[j]);
@@ -130,37 +157,51 @@ __global__ void __launch_bounds__(MAXT, 1) norm_fwd_kernel(const __grid_constant
       }
       s += part.x + part.y;
     }
-    fetch(base + stride + g);                  // in flight until the next turn
+    fetch(row + stride < p.rows);              // in flight until the next turn
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (p.h_out) put<VEC>(static_cast<TH*>(p.h_out) + r * p.ld_h_out, h[c], c, t, n, in_row);
-      if (p.h_ckpt) keep_chunk<VEC>(p.h_ckpt, p.ck, row, live, h[c], c, t, n);
+      if (FULL || p.h_out) put<VEC>(h_out, h[c], c, t, n, in_row);
+      if (!FULL && p.h_ckpt) keep_chunk<VEC>(p.h_ckpt, p.ck, row, live, h[c], c, t, n);
     }
-    if (!p.pre) {
-      if (p.post && row_warps > 1) __syncthreads();   // red[0] is read before the next row writes it
+    if (!pre) {
+      if (post && row_warps > 1) __syncthreads();     // red[0] is read before the next row writes it
       continue;
     }
-    const float r_pre = 1.f / sqrtf(fmaf(row_sum(s, red[1], row_warps), inv_n, p.eps));
+    const float r_pre = rsqrtf(fmaf(row_sum<SOLO>(s, red[1], row_warps), inv_n, p.eps));
     if (p.rstd_pre && live && t == 0) p.rstd_pre[row] = r_pre;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[c].p[j] = mul2(h[c].p[j], both(r_pre));
-      if (at.pre >= 0 && in[c]) {
+      if (w_pre && in[c]) {
         const F8 w = shared_vector<VEC>(vec + at.pre, c, t, n, cols);
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[c].p[j] = mul2(h[c].p[j], w.p[j]);
       }
-      if (p.x) put<VEC>(static_cast<TY*>(p.x) + r * p.ld_x, h[c], c, t, n, in_row);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[c].p[j] = mul2(h[c].p[j], both(r_pre));
+      if (FULL || p.x) put<VEC>(x, h[c], c, t, n, in_row);
       if (p.x_ckpt) keep_chunk<VEC>(p.x_ckpt, p.ck, row, live, h[c], c, t, n);
     }
-    if (!p.post && row_warps > 1) __syncthreads();    // likewise red[1]
+    if (!post && row_warps > 1) __syncthreads();      // likewise red[1]
   }
+}
+
+template <typename TH, typename TY, bool VEC, bool FULL>
+int launch_f(const NormParams& p, const FwdVectors& at, cudaStream_t s) {
+  const int threads = p.row_threads * p.rows_per_block, smem = at.floats * 4;
+  // two elements more a thread from 2048 columns on; registers for 3 x 256, 2 x 320 or one larger block an SM
+  auto* k = p.rows_per_block > 1 ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, false, FULL>
+            : p.row_threads * 8 >= p.cols ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, true, FULL>
+            : p.row_threads <= 320 ? norm_fwd_kernel<TH, TY, VEC, 2, 320, 2, true, FULL>
+            : p.row_threads <= 512 ? norm_fwd_kernel<TH, TY, VEC, 2, 512, 1, true, FULL>
+                                   : norm_fwd_kernel<TH, TY, VEC, 2, 1024, 1, true, FULL>;
+  const int per_sm = blocks_per_sm(reinterpret_cast<const void*>(k), threads, smem);
+  if (per_sm < 1) return CZ_ERR_CUDA;
+  const int64_t blocks = std::min<int64_t>(div_up(p.rows, p.rows_per_block), (int64_t)per_sm * sm_count());
+  return launch_kernel(k, dim3((unsigned)blocks), dim3((unsigned)threads), (size_t)smem, s, 1, p, at);
 }
 
 template <typename TH, typename TY, bool VEC>
 int launch_c(const NormParams& p, cudaStream_t s) {
-  const int threads = p.row_threads * p.rows_per_block;
   FwdVectors at{-1, -1, -1, 0};
   auto vector = [&](bool on) {
     if (!on) return int32_t{-1};
@@ -170,14 +211,9 @@ int launch_c(const NormParams& p, cudaStream_t s) {
   at.post = vector(p.post && p.w_post);
   at.pre = vector(p.pre && p.w_pre);
   at.gate = vector(p.gate_kind == kGateChannel);
-  const int smem = at.floats * 4;
-  auto* k = p.row_threads * 8 >= p.cols ? norm_fwd_kernel<TH, TY, VEC, 1, 512>
-            : p.row_threads <= 512 ? norm_fwd_kernel<TH, TY, VEC, 2, 512>
-                                   : norm_fwd_kernel<TH, TY, VEC, 2, 1024>;
-  const int per_sm = blocks_per_sm(reinterpret_cast<const void*>(k), threads, smem);
-  if (per_sm < 1) return CZ_ERR_CUDA;
-  const int64_t blocks = std::min<int64_t>(div_up(p.rows, p.rows_per_block), (int64_t)per_sm * sm_count());
-  return launch_kernel(k, dim3((unsigned)blocks), dim3((unsigned)threads), (size_t)smem, s, 1, p, at);
+  if constexpr (VEC && sizeof(TY) == 2)
+    if (at.post >= 0 && at.pre >= 0 && p.h_out && p.x && !p.h_ckpt && !p.y_ckpt) return launch_f<TH, TY, VEC, true>(p, at, s);
+  return launch_f<TH, TY, VEC, false>(p, at, s);
 }
 
 template <typename TH, typename TY>
