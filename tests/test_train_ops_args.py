@@ -116,3 +116,12 @@ def test_valid_arguments_without_a_device_are_unsupported_or_run():
     with pytest.raises(cz.CzError) as e:
         cz.cz_act_encode(x, ck)
     assert e.value.status in (cz.CZ_ERR_UNSUPPORTED, cz.CZ_ERR_CUDA)
+
+
+def test_norm_arguments_as_bytes_match_the_structure():
+    """The binding packs cz_norm_args in one go: every field lands where the structure has it."""
+    names = [n for n, _ in cz.cz_norm_args._fields_]
+    packed = cz._NORM_ARGS.pack(*range(1, len(names) + 1))
+    a = cz.cz_norm_args.from_buffer_copy(packed)
+    assert len(packed) == ctypes.sizeof(cz.cz_norm_args)
+    assert [int(getattr(a, n)) for n in names] == list(range(1, len(names) + 1))

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import List, Optional, Sequence, Tuple
 
 from . import build as _build
@@ -144,8 +145,8 @@ def load() -> ctypes.CDLL:
                                         _vp, ctypes.c_int32, _vp, ctypes.c_size_t, _vp]),
         "cz_norm_args_default": (None, [ctypes.POINTER(cz_norm_args)]),
         "cz_block_norm_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]),
-        "cz_block_norm_fwd": (ctypes.c_int, [ctypes.POINTER(cz_norm_args), _vp]),
-        "cz_block_norm_bwd": (ctypes.c_int, [ctypes.POINTER(cz_norm_args), _vp]),
+        "cz_block_norm_fwd": (ctypes.c_int, [_vp, _vp]),      # a cz_norm_args, as bytes or by reference
+        "cz_block_norm_bwd": (ctypes.c_int, [_vp, _vp]),
         "cz_token_logp_fwd": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                              ctypes.c_float, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp, _vp]),
         "cz_token_logp_bwd": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
@@ -505,7 +506,11 @@ def cz_act_size(rows: int, cols: int) -> int:
 
 
 def _ckpt(fn: str, name: str, t, rows: int, cols: int) -> Optional[int]:
-    return None if t is None else _bytes(fn, name, t, cz_act_size(rows, cols))
+    """Pointer of a checkpoint's buffer, which holds at least cz_act_size(rows, cols) bytes."""
+    if t is None:
+        return None
+    ld_q = (cols + 31) // 32 * 32
+    return _bytes(fn, name, t, (rows * ld_q + 127) // 128 * 128 + rows * ((ld_q // 32 + 15) // 16 * 16))
 
 
 def cz_act_encode(x, ckpt, stream=None) -> None:
@@ -564,28 +569,28 @@ def cz_block_norm_workspace(rows: int, cols: int) -> int:
     return n.value
 
 
+# cz_norm_args as bytes: one call in place of forty field assignments.
+_NORM_ARGS = struct.Struct("@2q6i3fi2P" + "Pq" * 3 + "2P" + "Pq" * 2 + "3P" + "Pq" * 5 + "2PPN")
+
+
 def _norm_common(fn, rows, cols, h_dtype, y_dtype, w_post, w_pre, gate, gate_act, h_scale, y_scale, eps, post_norm,
-                 pre_norm, rstd_post, rstd_pre):
-    for d in (h_dtype, y_dtype):
-        if torch.float32 and d not in _DTYPES:
-            raise CzError(fn, CZ_ERR_INVALID, f"type {d}: bfloat16 or float32 is wanted")
-    if gate_act not in GATE_ACTS:
+                 pre_norm, accumulate):
+    """The fields up to ld_gate."""
+    hd, yd = (_DTYPES.get(h_dtype, -1), _DTYPES.get(y_dtype, -1)) if torch.float32 else (-1, -1)
+    if hd < 0 or yd < 0:
+        raise CzError(fn, CZ_ERR_INVALID, f"types {h_dtype}, {y_dtype}: bfloat16 or float32 is wanted")
+    act = GATE_ACTS.get(gate_act)
+    if act is None:
         raise CzError(fn, CZ_ERR_INVALID, f"gate_act {gate_act!r}: one of {', '.join(GATE_ACTS)} is wanted")
-    a = cz_norm_args()
-    a.rows, a.cols = rows, cols
-    a.h_dtype, a.y_dtype = _DTYPES[h_dtype], _DTYPES[y_dtype]
-    a.post_norm, a.pre_norm = int(bool(post_norm)), int(bool(pre_norm))
-    a.h_scale, a.y_scale, a.eps = h_scale, y_scale, eps
-    a.w_post, a.w_pre = _vec(fn, "w_post", w_post, cols), _vec(fn, "w_pre", w_pre, cols)
-    a.rstd_post, a.rstd_pre = _vec(fn, "rstd_post", rstd_post, rows), _vec(fn, "rstd_pre", rstd_pre, rows)
+    kind, gp, ld_gate = 0, None, 0
     if gate is not None:
-        a.gate_act = GATE_ACTS[gate_act]
         if gate.dim() == 1:
-            a.gate_kind, a.gate = 1, _vec(fn, "gate", gate, cols)
+            kind, gp = 1, _vec(fn, "gate", gate, cols)
         else:
-            a.gate_kind = 2
-            a.gate, a.ld_gate = _mat(fn, "gate", gate, rows, cols, y_dtype)
-    return a
+            kind = 2
+            gp, ld_gate = _mat(fn, "gate", gate, rows, cols, y_dtype)
+    return (rows, cols, hd, yd, 1 if post_norm else 0, 1 if pre_norm else 0, kind, act, h_scale, y_scale, eps,
+            1 if accumulate else 0, _vec(fn, "w_post", w_post, cols) or 0, _vec(fn, "w_pre", w_pre, cols) or 0, gp or 0, ld_gate)
 
 
 def cz_block_norm_fwd(h, y, h_out=None, x=None, w_post=None, w_pre=None, gate=None, gate_act: str = "identity",
@@ -596,15 +601,19 @@ def cz_block_norm_fwd(h, y, h_out=None, x=None, w_post=None, w_pre=None, gate=No
     column, a 2-D gate (the type of y) one an element.  rstd_*, *_ckpt: written where given."""
     fn = "cz_block_norm_fwd"
     rows, cols = h.shape
-    a = _norm_common(fn, rows, cols, h.dtype, y.dtype, w_post, w_pre, gate, gate_act, h_scale, y_scale, eps, post_norm,
-                     pre_norm, rstd_post, rstd_pre)
-    a.h, a.ld_h = _mat(fn, "h", h, rows, cols)
-    a.y, a.ld_y = _mat(fn, "y", y, rows, cols)
-    a.h_out, a.ld_h_out = _mat(fn, "h_out", h_out, rows, cols, h.dtype)
-    a.x, a.ld_x = _mat(fn, "x", x, rows, cols, y.dtype)
-    a.h_ckpt, a.y_ckpt, a.x_ckpt = (_ckpt(fn, n, t, rows, cols) for n, t in
-                                    (("h_ckpt", h_ckpt), ("y_ckpt", y_ckpt), ("x_ckpt", x_ckpt)))
-    _check(fn, load().cz_block_norm_fwd(ctypes.byref(a), _stream_ptr(stream)))
+    ht, yt = h.dtype, y.dtype
+    first = _norm_common(fn, rows, cols, ht, yt, w_post, w_pre, gate, gate_act, h_scale, y_scale, eps, post_norm, pre_norm,
+                         False)
+    hp, ld_h = _mat(fn, "h", h, rows, cols)
+    yp, ld_y = _mat(fn, "y", y, rows, cols)
+    op, ld_o = _mat(fn, "h_out", h_out, rows, cols, ht)
+    xp, ld_x = _mat(fn, "x", x, rows, cols, yt)
+    args = _NORM_ARGS.pack(
+        *first, hp or 0, ld_h, yp or 0, ld_y, _vec(fn, "rstd_post", rstd_post, rows) or 0,
+        _vec(fn, "rstd_pre", rstd_pre, rows) or 0, op or 0, ld_o, xp or 0, ld_x, _ckpt(fn, "h_ckpt", h_ckpt, rows, cols) or 0,
+        _ckpt(fn, "y_ckpt", y_ckpt, rows, cols) or 0, _ckpt(fn, "x_ckpt", x_ckpt, rows, cols) or 0,
+        0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    _check(fn, load().cz_block_norm_fwd(args, _stream_ptr(stream)))
 
 
 def cz_block_norm_bwd(h, y, dx, dh_in, dh, dy, w_post=None, w_pre=None, gate=None, gate_act: str = "identity",
@@ -619,27 +628,29 @@ def cz_block_norm_bwd(h, y, dx, dh_in, dh, dy, w_post=None, w_pre=None, gate=Non
     if some is None:
         raise CzError(fn, CZ_ERR_INVALID, "no tensor gives the sizes")
     rows, cols = some.shape
-    h_type = next((t.dtype for t in (dh, dh_in, h) if t is not None), some.dtype)
-    y_type = next((t.dtype for t in (dy, dx, y) if t is not None), some.dtype)
-    a = _norm_common(fn, rows, cols, h_type, y_type, w_post, w_pre, gate, gate_act, h_scale, y_scale, 0.0, post_norm,
-                     pre_norm, rstd_post, rstd_pre)
-    a.accumulate = int(bool(accumulate))
-    a.h, a.ld_h = _mat(fn, "h", h, rows, cols, h_type)
-    a.y, a.ld_y = _mat(fn, "y", y, rows, cols, y_type)
-    a.h_ckpt, a.y_ckpt = _ckpt(fn, "h_ckpt", h_ckpt, rows, cols), _ckpt(fn, "y_ckpt", y_ckpt, rows, cols)
-    a.dx, a.ld_dx = _mat(fn, "dx", dx, rows, cols, y_type)
-    a.dh_in, a.ld_dh_in = _mat(fn, "dh_in", dh_in, rows, cols, h_type)
-    a.dh, a.ld_dh = _mat(fn, "dh", dh, rows, cols, h_type)
-    a.dy, a.ld_dy = _mat(fn, "dy", dy, rows, cols, y_type)
+    ht = next((t.dtype for t in (dh, dh_in, h) if t is not None), some.dtype)
+    yt = next((t.dtype for t in (dy, dx, y) if t is not None), some.dtype)
+    first = _norm_common(fn, rows, cols, ht, yt, w_post, w_pre, gate, gate_act, h_scale, y_scale, 0.0, post_norm, pre_norm,
+                         accumulate)
+    hp, ld_h = _mat(fn, "h", h, rows, cols, ht)
+    yp, ld_y = _mat(fn, "y", y, rows, cols, yt)
+    dxp, ld_dx = _mat(fn, "dx", dx, rows, cols, yt)
+    dip, ld_di = _mat(fn, "dh_in", dh_in, rows, cols, ht)
+    dhp, ld_dh = _mat(fn, "dh", dh, rows, cols, ht)
+    dyp, ld_dy = _mat(fn, "dy", dy, rows, cols, yt)
+    dgp, ld_dg = None, 0
     if dgate is not None:
         if gate is None or gate.dim() == 1:
-            a.dgate = _vec(fn, "dgate", dgate, cols)
+            dgp = _vec(fn, "dgate", dgate, cols)
         else:
-            a.dgate, a.ld_dgate = _mat(fn, "dgate", dgate, rows, cols, y_type)
-    a.dw_post, a.dw_pre = _vec(fn, "dw_post", dw_post, cols), _vec(fn, "dw_pre", dw_pre, cols)
-    if workspace is not None:
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(fn, load().cz_block_norm_bwd(ctypes.byref(a), _stream_ptr(stream)))
+            dgp, ld_dg = _mat(fn, "dgate", dgate, rows, cols, yt)
+    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    args = _NORM_ARGS.pack(
+        *first, hp or 0, ld_h, yp or 0, ld_y, _vec(fn, "rstd_post", rstd_post, rows) or 0,
+        _vec(fn, "rstd_pre", rstd_pre, rows) or 0, 0, 0, 0, 0, _ckpt(fn, "h_ckpt", h_ckpt, rows, cols) or 0,
+        _ckpt(fn, "y_ckpt", y_ckpt, rows, cols) or 0, 0, dxp or 0, ld_dx, dip or 0, ld_di, dhp or 0, ld_dh, dyp or 0, ld_dy,
+        dgp or 0, ld_dg, _vec(fn, "dw_post", dw_post, cols) or 0, _vec(fn, "dw_pre", dw_pre, cols) or 0, ws, ws_bytes)
+    _check(fn, load().cz_block_norm_bwd(args, _stream_ptr(stream)))
 
 
 def cz_token_logp_fwd(logits, targets, logp, entropy=None, lse=None, top_ids=None, top_logp=None,
