@@ -352,9 +352,13 @@ int cz_act_decode(const void* ckpt, int64_t rows, int64_t cols, void* x, int32_t
  * out: out_dtype, dense rows of n_in elements (a tensor of the flat gradient buffer,
  * fp32 or bf16, as the Muon step reads it); add: nullable, the same type and layout
  * (add == out accumulates in place).  Sums are fp32, out is rounded once.
- * workspace: >= cz_act_wgrad_workspace bytes, 256-byte aligned; its first 256 bytes
- * (the status word) must be zero before first use; cz_device_status(stream,
- * workspace) reads it.  Concurrent calls need workspaces of their own. */
+ * workspace: 256-byte aligned; its first 256 bytes (the status word) must be zero before
+ * first use; cz_device_status(stream, workspace) reads it.  cz_act_wgrad_workspace gives
+ * the bytes with which the call runs best: the checkpoint's values in bf16 (they are
+ * read once for every 256 rows of out), parts of the sums when out has few tiles, and a copy of dy
+ * if its rows do not start on 16-byte boundaries.  With less the call takes the columns in
+ * panels; it needs at least 256 + 128 * rows bytes and the copy of dy (2 * rows *
+ * round_up(n_out, 8), rounded up to 256).  Concurrent calls need workspaces of their own. */
 int cz_act_wgrad_workspace(const void* dy, int64_t ld_dy, int64_t rows, int64_t n_out, int64_t n_in, size_t* bytes);
 int cz_act_wgrad(const void* dy, int64_t ld_dy, const void* ckpt, int64_t rows, int64_t n_out, int64_t n_in,
                  const void* add, void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);

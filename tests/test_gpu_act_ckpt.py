@@ -133,6 +133,30 @@ def test_wgrad_many_tiles_and_a_long_sum():
     _wgrad_case(16384, 256, 264, "f32", None, seed=4)
 
 
+def test_wgrad_with_little_workspace_takes_panels():
+    """The smallest workspace (64 columns at a time), one for a panel and a half of tiles, and the recommended one: all right."""
+    rows, n_out, n_in = 700, 300, 1000
+    x, dy = torch.randn(rows, n_in, device="cuda"), torch.randn(rows, n_out, device="cuda").to(torch.bfloat16)
+    ck = _ckpt(rows, n_in)
+    cz.cz_act_encode(x, ck)
+    add = torch.randn(n_out, n_in, device="cuda")
+    xh = torch.empty_like(x)
+    cz.cz_act_decode(ck, xh)
+    d, xn = dy.double().cpu().numpy(), xh.double().cpu().numpy()
+    want = O.wgrad(d, xn, add.double().cpu().numpy())
+    tol = (rows / 16 + 16) * 2.0 ** -23 * (np.abs(d).T @ np.abs(xn) + np.abs(add.double().cpu().numpy()))
+    copy = -(-2 * rows * 304 // 256) * 256               # dy's rows are 600 bytes: not on 16-byte boundaries
+    least = 256 + copy + 128 * rows
+    for size in (least, least + 1000, 256 + copy + 2 * rows * 400, cz.cz_act_wgrad_workspace(dy, n_in)):
+        g = torch.empty(n_out, n_in, device="cuda")
+        ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+        cz.cz_act_wgrad(dy, ck, g, add=add, workspace=ws)
+        assert cz.cz_device_status(None, ws) == cz.CZ_OK
+        assert (np.abs(g.double().cpu().numpy() - want) <= tol).all()
+    with pytest.raises(cz.CzError):
+        cz.cz_act_wgrad(dy, ck, g, workspace=ws[:least - 1])
+
+
 def test_wgrad_of_no_rows_is_the_added_gradient():
     for add in (None, "other"):
         flat = _wgrad_case(0, 40, 72, "f32", add)

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) decode16_kernel(const uint8_t* __res
 template <typename T>
 __global__ void __launch_bounds__(kThreads) decode1_kernel(const uint8_t* __restrict__ ck, ActLayout l,
                                                            int64_t n_blocks, int cols, T* __restrict__ x, int64_t ld) {
-  const uint32_t per_row = (uint32_t)(l.ld_q / kActBlock);
+  const uint32_t per_row = (uint32_t)((cols + kActBlock - 1) / kActBlock);
   const int lane = threadIdx.x & 31;
   const int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnroll;
 #pragma unroll
@@ -170,21 +170,28 @@ int encode(const T* x, int64_t ld, int64_t rows, int64_t cols, uint8_t* ck, cuda
   return g ? launch_kernel(encode1_kernel<T>, g, kThreads, 0, s, 1, x, ld, n, (int)cols, ck, l) : CZ_ERR_UNSUPPORTED;
 }
 
+// Columns of a checkpoint from `ck` on, which is moved to the first of them (a multiple of 32), laid out as l.
 template <typename T>
-int decode(const uint8_t* ck, int64_t rows, int64_t cols, T* x, int64_t ld, cudaStream_t s) {
-  const ActLayout l = act_layout(rows, cols);
+int decode(const uint8_t* ck, const ActLayout& l, int64_t rows, int64_t cols, T* x, int64_t ld, cudaStream_t s) {
   if (cols % 8 == 0 && rows_aligned(x, ld, sizeof(T))) {
     const int64_t per_row = div_up(cols, 16);
     const unsigned g = blocks_for(rows * per_row, kThreads * kUnroll);
     return g ? launch_kernel(decode16_kernel<T>, g, kThreads, 0, s, 1, ck, l, rows, (uint32_t)cols, x, ld, step_of(per_row))
              : CZ_ERR_UNSUPPORTED;
   }
-  const int64_t n = rows * (l.ld_q / kActBlock);
+  const int64_t n = rows * div_up(cols, kActBlock);
   const unsigned g = blocks_for(n, kThreads / 32 * kUnroll);
   return g ? launch_kernel(decode1_kernel<T>, g, kThreads, 0, s, 1, ck, l, n, (int)cols, x, ld) : CZ_ERR_UNSUPPORTED;
 }
 
 }  // namespace
+
+int decode_columns(const void* ckpt, int64_t rows, int64_t cols, int64_t first, int64_t n, __nv_bfloat16* x, int64_t ld,
+                   cudaStream_t s) {
+  ActLayout l = act_layout(rows, cols);
+  l.e_off += first / kActBlock - first;      // seen from the moved pointer
+  return decode(static_cast<const uint8_t*>(ckpt) + first, l, rows, n, x, ld, s);
+}
 
 int check_sm103() {
   static thread_local int known_dev = -1, known = CZ_OK;
@@ -268,6 +275,7 @@ extern "C" int cz_act_decode(const void* ckpt, int64_t rows, int64_t cols, void*
   cz::NvtxRange range("cz/act_decode");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const uint8_t* ck = static_cast<const uint8_t*>(ckpt);
-  return dtype == CZ_F32 ? cz::decode(ck, rows, cols, static_cast<float*>(x), ld, s)
-                         : cz::decode(ck, rows, cols, static_cast<__nv_bfloat16*>(x), ld, s);
+  const cz::ActLayout l = cz::act_layout(rows, cols);
+  return dtype == CZ_F32 ? cz::decode(ck, l, rows, cols, static_cast<float*>(x), ld, s)
+                         : cz::decode(ck, l, rows, cols, static_cast<__nv_bfloat16*>(x), ld, s);
 }

@@ -2,6 +2,7 @@
 // checkpoints, block norms, token log probabilities).  Not part of the C-ABI.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -35,6 +36,10 @@ inline bool matrix_ok(const void* p, int64_t rows, int64_t cols, int64_t ld, int
 inline bool rows_aligned(const void* p, int64_t ld, int64_t bytes) {
   return p == nullptr || (aligned(p, 16) && (ld * bytes) % 16 == 0);
 }
+
+// bf16 values of columns [first, first + n) of a checkpoint of rows x cols (first: a multiple of 64).
+int decode_columns(const void* ckpt, int64_t rows, int64_t cols, int64_t first, int64_t n, __nv_bfloat16* x, int64_t ld,
+                   cudaStream_t s);
 
 // CZ_OK on an sm_103 device; the answer is looked up once per device.
 int check_sm103();
