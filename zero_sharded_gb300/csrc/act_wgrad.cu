@@ -7,7 +7,7 @@
 // (cta_group::2) a tile computes 256 x 256 of out^T, M = 256 columns k of out, N = 256 rows n, in steps of 64 tokens,
 // both operands MN-major in shared memory (the sum runs over their rows).  Decoding inside the product (from
 // shared memory to TMEM as the A operand) reads half the bytes but repeats itself for every 256 rows
-// of out, on issue slots and under the power cap that the products need: 1.51 ms against XXX at
+// of out, on issue slots and under the power cap that the products need: 1.51 ms against 1.39 at
 // 8192 x 25600 x 5120.
 //
 // The tensor core truncates when it adds to an accumulator, an error of about 1e-8 of the sum for
@@ -60,6 +60,7 @@ struct WgradParams {
   int32_t nk;                // steps of a whole tile
   int32_t splits, per_split; // parts of the sum of a tile, and their steps
   int64_t split_stride;      // elements of `out` from part to part
+  int32_t height;            // rows of out a tile (the accumulator's columns)
   int32_t tiles_m, tiles_n;  // tiles over n_out and the panel
   int32_t units;             // CTA pairs
   int32_t out_f32;
@@ -104,13 +105,13 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
   return s;
 }
 
-// 128 columns of the accumulator: lane = column k of out, v[j] = row n0 + j.
+// Half of the accumulator's columns: lane = column k of out, v[j] = row n0 + j.
 template <typename TO>
 __device__ __forceinline__ void store_columns(const WgradParams& p, const float* v, int64_t n0, int64_t k, int64_t part) {
   if (k >= p.n_in) return;
   const TO* add = static_cast<const TO*>(p.add);
   TO* out = static_cast<TO*>(p.out) + part + n0 * p.ld + k;
-  const int rows = (int)min((int64_t)128, p.n_out - n0);
+  const int rows = (int)min((int64_t)(p.height / 2), p.n_out - n0);
   if (add) {
     add += n0 * p.ld + k;
     constexpr int kBatch = 16;
@@ -179,7 +180,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
       bool ok = true;
       for (int t = unit; ok && t < items; t += p.units) {
         const Item it = item_at(p, t);
-        const int n0 = it.tm * kTile + (int)rank * 128, k0 = it.tn * kTile + (int)rank * 128;
+        const int n0 = it.tm * p.height + (int)rank * (p.height / 2), k0 = it.tn * kTile + (int)rank * 128;
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
           if (!mbar_poll(&sm.done[stage], phase ^ 1u, abort, status, kTimeoutClocks)) {
             ok = false;
@@ -208,7 +209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
           if (issued & (1u << s)) mbar_poll(&sm.full[s], (last_par >> s) & 1u, nullptr, status, kTimeoutClocks);
     } else if (warp == 1 && rank == 0 && lane == 0) {
       // ---------------------------------------------------------- MMA issuer (even CTA)
-      constexpr uint32_t idesc = idesc_bf16_f32_bmn(kTile, kTile) | (1u << 15);   // both operands MN-major
+      const uint32_t idesc = idesc_bf16_f32_bmn(kTile, p.height) | (1u << 15);   // both operands MN-major
       const uint64_t da0 = sdesc_mnmajor_sw128(smem_u32(sm.stage), kBytesA / 2, 1024);
       const uint64_t db0 = sdesc_mnmajor_sw128(smem_u32(sm.stage) + kBytesA, kBytesB / 2, 1024);
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
@@ -259,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
     for (int t = unit; ok && t < items; t += p.units) {
       const Item it = item_at(p, t);
       const int64_t k = (int64_t)it.tn * kTile + rank * 128 + quad * 32 + lane;
-      const int64_t n0 = (int64_t)it.tm * kTile + half * 128;
+      const int64_t n0 = (int64_t)it.tm * p.height + half * (p.height / 2);
       float v[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) v[j] = 0.f;
@@ -270,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wgrad_k
           break;
         }
         tc_fence_after();
-        const uint32_t from = tmem + acc * (uint32_t)kTile + half * 128 + lanes;
+        const uint32_t from = tmem + acc * (uint32_t)kTile + half * (p.height / 2) + lanes;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float a[32];
@@ -378,10 +379,33 @@ int join(const float* part, int parts, int64_t rows, int64_t n, const void* add,
                        static_cast<TO*>(out), ld);
 }
 
-// Parts of every tile's sum when there are fewer tiles than units: as many as keep the units busy, with at
-// least kChunk steps each (16 parts at most).
-int splits_for(int64_t tiles, int64_t nk, int64_t units) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, units / tiles, nk / kChunk}));
+// How a panel is cut: rows of out a tile, and parts of every tile's sum.  A step of a tile of height h keeps shared
+// memory busy for 256 + h clocks (copies in and operands out, 128 bytes a clock), the tensor cores for 2 h.  All
+// units finish after the rounds that the slowest one has, so a lower tile can be the better fit (192 tiles of 256 on
+// 76 units are 3 rounds of 512 clocks a step, 224 of 224 are 3 of 480), and where there are fewer tiles than
+// units their sums are split, at least kChunk steps a part, which costs a join.  Measured, tiles of 256
+// unsplit / this rule (rows x n_out x n_in): 16384 x 512 x 512 84.6 / 31.2 us, 8192 x 1024 x 2048 56.1 / 52.0,
+// 2048 x 2048 x 1024 25.1 / 23.1, 4096 x 4096 x 2560 78.3 / 74.2, 4097 x 6144 x 2048 78.4 / 76.4.
+struct Cut {
+  int64_t height, splits;
+};
+Cut cut_for(int64_t n_out, int64_t n_in, int64_t nk, int64_t units) {
+  Cut best{kTile, 1};
+  double least = 0;
+  for (int64_t h = kTile; h >= 128; h -= 32) {
+    const int64_t tiles = div_up(n_out, h) * div_up(n_in, kTile);
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, units / tiles, nk / kChunk}));
+    for (int64_t s : {int64_t{1}, parts}) {
+      const int64_t per = round_up(div_up(nk, s), s > 1 ? kChunk : 1);
+      double clocks = (double)(div_up(tiles * div_up(nk, per), units) * per * (256 + h));
+      if (s > 1) clocks += 6000 + (double)(s * n_out * n_in) * 8 / 3400;   // a launch, and the parts out and in
+      if (least == 0 || clocks < 0.97 * least) {
+        least = clocks;
+        best = Cut{h, s};
+      }
+    }
+  }
+  return best;
 }
 
 template <typename TO>
@@ -411,8 +435,7 @@ int64_t panel_bytes(int64_t rows, int64_t cols) { return rows * cols * 2; }
 extern "C" int cz_act_wgrad_workspace(const void* dy, int64_t ld_dy, int64_t rows, int64_t n_out, int64_t n_in,
                                       size_t* bytes) {
   if (!bytes || !sizes_ok(rows, n_out, n_in) || !matrix_ok(dy, rows, n_out, ld_dy, 2)) return CZ_ERR_INVALID;
-  const int64_t tiles = div_up(n_out, kTile) * div_up(n_in, kTile);
-  const int splits = splits_for(tiles, div_up(rows, kDepth), kUnits);
+  const int64_t splits = rows > 0 ? cut_for(n_out, n_in, div_up(rows, kDepth), kUnits).splits : 1;
   *bytes = (size_t)(before_panel(dy, ld_dy, rows, n_out) + round_up(panel_bytes(rows, round_up(n_in, kPanel)), 256) +
                     (splits > 1 ? splits * n_out * n_in * 4 : 0));
   return CZ_OK;
@@ -425,8 +448,7 @@ extern "C" int cz_act_wgrad(const void* dy, int64_t ld_dy, const void* ckpt, int
   if (!is_dtype(out_dtype) || !out || !aligned(out, dtype_bytes(out_dtype)) || !aligned(add, dtype_bytes(out_dtype)) ||
       (!ckpt && rows > 0) || !aligned(ckpt, 16))
     return CZ_ERR_INVALID;
-  const int64_t tiles_m = div_up(n_out, kTile);
-  if (tiles_m * div_up(n_in, kTile) > INT32_MAX / 2) return CZ_ERR_INVALID;
+  if (div_up(n_out, 128) * div_up(n_in, kTile) > INT32_MAX / kMaxSplits) return CZ_ERR_INVALID;
   const uintptr_t o0 = reinterpret_cast<uintptr_t>(out), a0 = reinterpret_cast<uintptr_t>(add);
   const uintptr_t span = (uintptr_t)(n_out * n_in * dtype_bytes(out_dtype));
   if (add && a0 != o0 && a0 < o0 + span && o0 < a0 + span) return CZ_ERR_INVALID;   // part of add would be overwritten
@@ -460,7 +482,6 @@ extern "C" int cz_act_wgrad(const void* dy, int64_t ld_dy, const void* ckpt, int
   p.status = reinterpret_cast<int32_t*>(ws);
   p.n_out = n_out;
   p.nk = (int32_t)div_up(rows, kDepth);
-  p.tiles_m = (int32_t)tiles_m;
   if (!encode_map(&p.dy, dy, n_out, rows, ld_dy)) return CZ_ERR_CUDA;
   const int64_t b = dtype_bytes(out_dtype);
   for (int64_t k0 = 0; k0 < n_in; k0 += cols) {
@@ -472,11 +493,15 @@ extern "C" int cz_act_wgrad(const void* dy, int64_t ld_dy, const void* ckpt, int
     const void* const add_k = add ? static_cast<const uint8_t*>(add) + k0 * b : nullptr;
     void* const out_k = static_cast<uint8_t*>(out) + k0 * b;
     p.tiles_n = (int32_t)div_up(p.n_in, kTile);
-    const int64_t tiles = tiles_m * p.tiles_n, panel = round_up(panel_bytes(rows, ld_x), 256);
+    const int64_t panel = round_up(panel_bytes(rows, ld_x), 256);
     // parts of the sums lie behind the panel
     float* const parts = reinterpret_cast<float*>(ws + before + panel);
-    p.splits = (int)std::min<int64_t>(splits_for(tiles, p.nk, units), std::max<int64_t>(1, (room - panel) / (n_out * p.n_in * 4)));
-    p.per_split = (int32_t)round_up(div_up(p.nk, p.splits), kChunk);
+    const Cut cut = cut_for(n_out, p.n_in, p.nk, units);
+    p.height = (int32_t)cut.height;
+    p.tiles_m = (int32_t)div_up(n_out, cut.height);
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    p.splits = (int32_t)std::min<int64_t>(cut.splits, std::max<int64_t>(1, (room - panel) / (n_out * p.n_in * 4)));
+    p.per_split = (int32_t)round_up(div_up(p.nk, p.splits), p.splits > 1 ? kChunk : 1);
     p.splits = (int32_t)div_up(p.nk, p.per_split);
     const bool split = p.splits > 1;
     p.add = split ? nullptr : add_k;
