@@ -18,9 +18,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
+constexpr int kWarps = kThreads / 32, kUnroll1 = 8;
 
-// Where a thread is: item i of a matrix with per_row items a row.  One division at the start; the next item, kThreads
-// further, is `rows` rows and `items` items on.
+// Where a thread is: item i of a matrix with per_row items a row.  One division at the start; its next item is `rows`
+// rows and `items` items on.
 struct Step {
   uint32_t rows, items;
 };
@@ -74,29 +75,31 @@ __global__ void __launch_bounds__(kThreads) encode8_kernel(const T* __restrict__
   }
 }
 
+// A block of 32 an item, one element a lane.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) encode1_kernel(const T* __restrict__ x, int64_t ld, int64_t n_blocks,
-                                                           int cols, uint8_t* __restrict__ ck, ActLayout l) {
-  const uint32_t per_row = (uint32_t)(l.ld_q / kActBlock);
-  const int lane = threadIdx.x & 31;
-  const int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnroll;
-  float v[kUnroll];
+__global__ void __launch_bounds__(kThreads) encode1_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, uint32_t cols,
+                                                           uint8_t* __restrict__ ck, ActLayout l, Step step) {
+  const uint32_t per_row = (uint32_t)(l.ld_q / kActBlock), lane = threadIdx.x & 31;
+  const At first((int64_t)blockIdx.x * (kWarps * kUnroll1) + (threadIdx.x >> 5), per_row);
+  T v[kUnroll1];
+  At at = first;
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = i0 + u, row = i / per_row;
-    const int c = (int)(i - row * per_row) * kActBlock + lane;
-    v[u] = (i < n_blocks && c < cols) ? load1(x + row * ld + c) : 0.f;
+  for (int u = 0; u < kUnroll1; ++u) {
+    const uint32_t c = at.item * kActBlock + lane;
+    v[u] = T(0.f);
+    if (at.row < rows && c < cols) v[u] = x[at.row * ld + c];
+    at.next(step, per_row);
   }
+  at = first;
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = i0 + u, row = i / per_row;
+  for (int u = 0; u < kUnroll1; ++u) {
     uint32_t q;
-    const uint32_t b = act_encode1(v[u], &q);
-    if (i < n_blocks) {
-      const int blk = (int)(i - row * per_row);
-      ck[row * l.ld_q + blk * kActBlock + lane] = (uint8_t)q;
-      if (lane == 0) ck[l.e_off + row * l.ld_e + blk] = (uint8_t)b;
+    const uint32_t b = act_encode1((float)v[u], &q);
+    if (at.row < rows) {
+      ck[at.row * l.ld_q + at.item * kActBlock + lane] = (uint8_t)q;
+      if (lane == 0) ck[l.e_off + at.row * l.ld_e + at.item] = (uint8_t)b;
     }
+    at.next(step, per_row);
   }
 }
 
@@ -132,17 +135,26 @@ __global__ void __launch_bounds__(kThreads) decode16_kernel(const uint8_t* __res
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) decode1_kernel(const uint8_t* __restrict__ ck, ActLayout l,
-                                                           int64_t n_blocks, int cols, T* __restrict__ x, int64_t ld) {
-  const uint32_t per_row = (uint32_t)((cols + kActBlock - 1) / kActBlock);
-  const int lane = threadIdx.x & 31;
-  const int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnroll;
+__global__ void __launch_bounds__(kThreads) decode1_kernel(const uint8_t* __restrict__ ck, ActLayout l, int64_t rows, uint32_t cols,
+                                                           T* __restrict__ x, int64_t ld, Step step) {
+  const uint32_t per_row = (cols + kActBlock - 1) / kActBlock, lane = threadIdx.x & 31;
+  const At first((int64_t)blockIdx.x * (kWarps * kUnroll1) + (threadIdx.x >> 5), per_row);
+  uint8_t q[kUnroll1], b[kUnroll1];
+  At at = first;
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = i0 + u, row = i / per_row;
-    const int blk = (int)(i - row * per_row), c = blk * kActBlock + lane;
-    if (i < n_blocks && c < cols)
-      store1(x + row * ld + c, act_decode1(ck[row * l.ld_q + c], ck[l.e_off + row * l.ld_e + blk]));
+  for (int u = 0; u < kUnroll1; ++u) {
+    if (at.row < rows) {
+      q[u] = ck[at.row * l.ld_q + at.item * kActBlock + lane];
+      b[u] = ck[l.e_off + at.row * l.ld_e + at.item];
+    }
+    at.next(step, per_row);
+  }
+  at = first;
+#pragma unroll
+  for (int u = 0; u < kUnroll1; ++u) {
+    const uint32_t c = at.item * kActBlock + lane;
+    if (at.row < rows && c < cols) store1(x + at.row * ld + c, act_decode1(q[u], b[u]));
+    at.next(step, per_row);
   }
 }
 
@@ -154,7 +166,7 @@ unsigned blocks_for(int64_t n, int64_t per_block) {
   return b > INT32_MAX ? 0u : (unsigned)b;
 }
 
-Step step_of(int64_t per_row) { return Step{(uint32_t)(kThreads / per_row), (uint32_t)(kThreads % per_row)}; }
+Step step_of(int64_t per_row, int64_t items) { return Step{(uint32_t)(items / per_row), (uint32_t)(items % per_row)}; }
 
 template <typename T>
 int encode(const T* x, int64_t ld, int64_t rows, int64_t cols, uint8_t* ck, cudaStream_t s) {
@@ -162,12 +174,13 @@ int encode(const T* x, int64_t ld, int64_t rows, int64_t cols, uint8_t* ck, cuda
   if (cols % 8 == 0 && rows_aligned(x, ld, sizeof(T))) {
     const int64_t per_row = l.ld_q / 8;
     const unsigned g = blocks_for(rows * per_row, kThreads * kUnroll);
-    return g ? launch_kernel(encode8_kernel<T>, g, kThreads, 0, s, 1, x, ld, rows, (uint32_t)cols, ck, l, step_of(per_row))
+    return g ? launch_kernel(encode8_kernel<T>, g, kThreads, 0, s, 1, x, ld, rows, (uint32_t)cols, ck, l, step_of(per_row, kThreads))
              : CZ_ERR_UNSUPPORTED;
   }
-  const int64_t n = rows * (l.ld_q / kActBlock);
-  const unsigned g = blocks_for(n, kThreads / 32 * kUnroll);
-  return g ? launch_kernel(encode1_kernel<T>, g, kThreads, 0, s, 1, x, ld, n, (int)cols, ck, l) : CZ_ERR_UNSUPPORTED;
+  const int64_t per_row = l.ld_q / kActBlock;
+  const unsigned g = blocks_for(rows * per_row, kWarps * kUnroll1);
+  return g ? launch_kernel(encode1_kernel<T>, g, kThreads, 0, s, 1, x, ld, rows, (uint32_t)cols, ck, l, step_of(per_row, kWarps))
+           : CZ_ERR_UNSUPPORTED;
 }
 
 // Columns of a checkpoint from `ck` on, which is moved to the first of them (a multiple of 32), laid out as l.
@@ -176,12 +189,13 @@ int decode(const uint8_t* ck, const ActLayout& l, int64_t rows, int64_t cols, T*
   if (cols % 8 == 0 && rows_aligned(x, ld, sizeof(T))) {
     const int64_t per_row = div_up(cols, 16);
     const unsigned g = blocks_for(rows * per_row, kThreads * kUnroll);
-    return g ? launch_kernel(decode16_kernel<T>, g, kThreads, 0, s, 1, ck, l, rows, (uint32_t)cols, x, ld, step_of(per_row))
+    return g ? launch_kernel(decode16_kernel<T>, g, kThreads, 0, s, 1, ck, l, rows, (uint32_t)cols, x, ld, step_of(per_row, kThreads))
              : CZ_ERR_UNSUPPORTED;
   }
-  const int64_t n = rows * div_up(cols, kActBlock);
-  const unsigned g = blocks_for(n, kThreads / 32 * kUnroll);
-  return g ? launch_kernel(decode1_kernel<T>, g, kThreads, 0, s, 1, ck, l, n, (int)cols, x, ld) : CZ_ERR_UNSUPPORTED;
+  const int64_t per_row = div_up(cols, kActBlock);
+  const unsigned g = blocks_for(rows * per_row, kWarps * kUnroll1);
+  return g ? launch_kernel(decode1_kernel<T>, g, kThreads, 0, s, 1, ck, l, rows, (uint32_t)cols, x, ld, step_of(per_row, kWarps))
+           : CZ_ERR_UNSUPPORTED;
 }
 
 }  // namespace

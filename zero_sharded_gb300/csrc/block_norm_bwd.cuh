@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   __shared__ float red[2][64];
   extern __shared__ __align__(16) uint8_t dyn[];
   constexpr bool BULK = RING && VEC;
-  const int n = SOLO ? (int)blockDim.x : p.row_threads;
+  const int n = !SOLO ? p.row_threads : VEC ? (int)blockDim.x : MAXT;   // fixed distances where elements move singly
   const int groups = SOLO ? 1 : p.rows_per_block;
   const int g = SOLO ? 0 : threadIdx.x / n, t = threadIdx.x - g * n, row_warps = n >> 5;
   const float inv_n = 1.f / (float)p.cols;
@@ -544,16 +544,19 @@ BwdLayout layout_of(const NormParams& p, int h_bytes, int y_bytes, int64_t room)
 }
 
 template <typename TH, typename TY, bool VEC, bool CHANNEL, int MODE>
-int launch_ring(const NormParams& p, const BwdLayout& l, int blocks, cudaStream_t s) {
+int launch_ring(NormParams p, const BwdLayout& l, int blocks, cudaStream_t s) {
   const bool solo = p.rows_per_block == 1;
   const int64_t fold = solo ? 0 : (int64_t)sizeof(float) * p.rows_per_block * round_up(p.cols, 4);
   const int64_t smem = std::max<int64_t>(fold, l.vectors * 4 + (int64_t)round_ring(l) * p.rows_per_block);
+  const int most = p.row_threads <= 256 ? 256 : p.row_threads <= 640 ? 640 : 1024;
   auto* k = !solo ? norm_bwd_kernel<TH, TY, VEC, 1, 256, false, true, CHANNEL, MODE>
-            : p.row_threads > 256 && p.row_threads <= 640 ? norm_bwd_kernel<TH, TY, VEC, 1, 640, true, true, CHANNEL, MODE>
-            : p.row_threads <= 256 ? norm_bwd_kernel<TH, TY, VEC, 1, 256, true, true, CHANNEL, MODE>
-                                   : norm_bwd_kernel<TH, TY, VEC, 1, 1024, true, true, CHANNEL, MODE>;
-  if (blocks_per_sm(reinterpret_cast<const void*>(k), p.row_threads * p.rows_per_block, (int)smem) < 1) return CZ_ERR_CUDA;
-  return launch_kernel(k, dim3((unsigned)blocks), dim3((unsigned)(p.row_threads * p.rows_per_block)), (size_t)smem, s, 1, p, l);
+            : most == 256 ? norm_bwd_kernel<TH, TY, VEC, 1, 256, true, true, CHANNEL, MODE>
+            : most == 640 ? norm_bwd_kernel<TH, TY, VEC, 1, 640, true, true, CHANNEL, MODE>
+                          : norm_bwd_kernel<TH, TY, VEC, 1, 1024, true, true, CHANNEL, MODE>;
+  if (solo && !VEC) p.row_threads = most;
+  const int threads = p.row_threads * p.rows_per_block;
+  if (blocks_per_sm(reinterpret_cast<const void*>(k), threads, (int)smem) < 1) return CZ_ERR_CUDA;
+  return launch_kernel(k, dim3((unsigned)blocks), dim3((unsigned)threads), (size_t)smem, s, 1, p, l);
 }
 
 template <typename TH, typename TY, bool VEC, bool CHANNEL>
@@ -561,7 +564,7 @@ int launch_c(NormParams p, int blocks, cudaStream_t s) {
   const BwdLayout l = layout_of(p, sizeof(TH), sizeof(TY), norm_bwd_room(p));
   if (l.stages == 0 || p.cols > 8 * 1024) {   // rows too wide: 16 elements a thread, straight from memory
     BwdLayout none{};
-    p.row_threads = (int32_t)round_up(div_up(p.cols, 16), 32);
+    p.row_threads = VEC ? (int32_t)round_up(div_up(p.cols, 16), 32) : 1024;
     return launch_kernel(norm_bwd_kernel<TH, TY, VEC, 2, 1024, true, false, CHANNEL, kAny>, dim3((unsigned)blocks),
                          dim3((unsigned)p.row_threads), 0, s, 1, p, none);
   }

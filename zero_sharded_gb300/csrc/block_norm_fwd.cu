@@ -60,12 +60,14 @@ __device__ __forceinline__ float row_sum(float v, float* red, int row_warps) {
   return v;
 }
 
-// SOLO: a row a block.  FULL: both norms with weights, h' and x wanted, of the checkpoints at most x's.
+// SOLO: a row a block.  FULL: both norms with weights, h' and x wanted, of the checkpoints at most x's.  Rows at any
+// alignment (no VEC) move element by element; with MAXT threads, known when compiling, the
+// elements of a thread lie at fixed distances (16 in place of 96 instructions an element).
 template <typename TH, typename TY, bool VEC, int C, int MAXT, int MINB, bool SOLO, bool FULL>
 __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const __grid_constant__ NormParams p, const FwdVectors at) {
   __shared__ float red[2][32];
   extern __shared__ __align__(16) float vec[];
-  const int n = SOLO ? (int)blockDim.x : p.row_threads;
+  const int n = !SOLO ? p.row_threads : VEC ? (int)blockDim.x : MAXT;
   const int g = SOLO ? 0 : threadIdx.x / n, t = threadIdx.x - g * n, row_warps = n >> 5;
   const int groups = SOLO ? 1 : p.rows_per_block;
   const int cols = p.cols;
@@ -186,14 +188,18 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const __grid_const
 }
 
 template <typename TH, typename TY, bool VEC, bool FULL>
-int launch_f(const NormParams& p, const FwdVectors& at, cudaStream_t s) {
+int launch_f(NormParams p, const FwdVectors& at, cudaStream_t s) {
+  const bool solo = p.rows_per_block == 1;
+  const int per_thread = p.row_threads * 8 >= p.cols ? 1 : 2;
+  // two chunks a thread from 2048 columns on; registers for 3 x 256, 2 x 320 or one larger block an SM
+  const int most = !solo || per_thread == 1 ? 256 : p.row_threads <= 320 ? 320 : p.row_threads <= 512 ? 512 : 1024;
+  auto* k = !solo ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, false, FULL>
+            : per_thread == 1 ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, true, FULL>
+            : most == 320 ? norm_fwd_kernel<TH, TY, VEC, 2, 320, 2, true, FULL>
+            : most == 512 ? norm_fwd_kernel<TH, TY, VEC, 2, 512, 1, true, FULL>
+                          : norm_fwd_kernel<TH, TY, VEC, 2, 1024, 1, true, FULL>;
+  if (solo && !VEC) p.row_threads = most;
   const int threads = p.row_threads * p.rows_per_block, smem = at.floats * 4;
-  // two elements more a thread from 2048 columns on; registers for 3 x 256, 2 x 320 or one larger block an SM
-  auto* k = p.rows_per_block > 1 ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, false, FULL>
-            : p.row_threads * 8 >= p.cols ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, true, FULL>
-            : p.row_threads <= 320 ? norm_fwd_kernel<TH, TY, VEC, 2, 320, 2, true, FULL>
-            : p.row_threads <= 512 ? norm_fwd_kernel<TH, TY, VEC, 2, 512, 1, true, FULL>
-                                   : norm_fwd_kernel<TH, TY, VEC, 2, 1024, 1, true, FULL>;
   const int per_sm = blocks_per_sm(reinterpret_cast<const void*>(k), threads, smem);
   if (per_sm < 1) return CZ_ERR_CUDA;
   const int64_t blocks = std::min<int64_t>(div_up(p.rows, p.rows_per_block), (int64_t)per_sm * sm_count());
