@@ -1,9 +1,9 @@
 // Writing and reading 8-bit activation checkpoints (format: act_ckpt.cuh).
 //
 // Both directions are one pass over memory: s + 33/32 bytes an element (s = 2 for bf16,
-// 4 for fp32).  Rows on 16-byte boundaries take 8 elements at a time (16 when reading), a block of 32 being
-// 4 lanes; other strides take one element a lane, a block being a warp (one warp-wide
-// integer maximum), so that loads stay coalesced at any alignment.
+// 4 for fp32).  A thread takes 8 consecutive elements at a time (16 when it writes aligned rows), a block of 32
+// being 4 lanes.  Rows that do not start on 16-byte boundaries are shifted into place after aligned loads, and
+// written in words through shared memory.
 
 #include <cuda_runtime.h>
 
@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
-constexpr int kWarps = kThreads / 32, kUnroll1 = 8;
+constexpr int kWarps = kThreads / 32;
 
 // Where a thread is: item i of a matrix with per_row items a row.  One division at the start; its next item is `rows`
 // rows and `items` items on.
@@ -48,56 +48,36 @@ struct At {
   }
 };
 
-// 8 elements an item.
-template <typename T>
+// 8 elements an item; VEC: every item lies on a 16-byte boundary.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) encode8_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, uint32_t cols,
                                                            uint8_t* __restrict__ ck, ActLayout l, Step step) {
   const uint32_t per_row = (uint32_t)(l.ld_q / 8);
   const At first((int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x, per_row);
-  Raw8<T> raw[kUnroll];
+  Raw8<T> raw[VEC ? kUnroll : 1];
+  RawAny<T> any[VEC ? 1 : kUnroll];
   At at = first;
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    zero8(raw[u]);
-    if (at.row < rows && at.item * 8 < cols) load8(x + at.row * ld + at.item * 8, raw[u]);   // cols % 8 == 0 here
-    at.next(step, per_row);
-  }
-  at = first;
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const uint32_t b = act_block_scale(act_amax8(raw[u]));
-    const uint2 q = act_pack8(values(raw[u]), b);
-    if (at.row < rows) {
-      *reinterpret_cast<uint2*>(ck + at.row * l.ld_q + at.item * 8) = q;
-      if ((threadIdx.x & 3) == 0) ck[l.e_off + at.row * l.ld_e + at.item / 4] = (uint8_t)b;
+    if constexpr (VEC) {
+      zero8(raw[u]);
+      if (at.row < rows && at.item * 8 < cols) load8(x + at.row * ld + at.item * 8, raw[u]);
+    } else {
+      load8_any(any[u], x + at.row * ld, at.row, Extent{rows, ld}, (int)at.item * 8, at.row < rows ? (int)cols : 0);
     }
     at.next(step, per_row);
   }
-}
-
-// A block of 32 an item, one element a lane.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) encode1_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, uint32_t cols,
-                                                           uint8_t* __restrict__ ck, ActLayout l, Step step) {
-  const uint32_t per_row = (uint32_t)(l.ld_q / kActBlock), lane = threadIdx.x & 31;
-  const At first((int64_t)blockIdx.x * (kWarps * kUnroll1) + (threadIdx.x >> 5), per_row);
-  T v[kUnroll1];
-  At at = first;
-#pragma unroll
-  for (int u = 0; u < kUnroll1; ++u) {
-    const uint32_t c = at.item * kActBlock + lane;
-    v[u] = T(0.f);
-    if (at.row < rows && c < cols) v[u] = x[at.row * ld + c];
-    at.next(step, per_row);
-  }
   at = first;
 #pragma unroll
-  for (int u = 0; u < kUnroll1; ++u) {
-    uint32_t q;
-    const uint32_t b = act_encode1((float)v[u], &q);
+  for (int u = 0; u < kUnroll; ++u) {
+    Raw8<T> r;
+    if constexpr (VEC) r = raw[u];
+    else r = raw8(any[u], (int)at.item * 8, at.row < rows ? (int)cols : 0);
+    const uint32_t b = act_block_scale(act_amax8(r));
+    const uint2 q = act_pack8(values(r), b);
     if (at.row < rows) {
-      ck[at.row * l.ld_q + at.item * kActBlock + lane] = (uint8_t)q;
-      if (lane == 0) ck[l.e_off + at.row * l.ld_e + at.item] = (uint8_t)b;
+      *reinterpret_cast<uint2*>(ck + at.row * l.ld_q + at.item * 8) = q;
+      if ((threadIdx.x & 3) == 0) ck[l.e_off + at.row * l.ld_e + at.item / 4] = (uint8_t)b;
     }
     at.next(step, per_row);
   }
@@ -134,26 +114,32 @@ __global__ void __launch_bounds__(kThreads) decode16_kernel(const uint8_t* __res
   }
 }
 
+// Rows at any alignment: 256 elements of a row a warp, which writes them through shared memory.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) decode1_kernel(const uint8_t* __restrict__ ck, ActLayout l, int64_t rows, uint32_t cols,
-                                                           T* __restrict__ x, int64_t ld, Step step) {
-  const uint32_t per_row = (cols + kActBlock - 1) / kActBlock, lane = threadIdx.x & 31;
-  const At first((int64_t)blockIdx.x * (kWarps * kUnroll1) + (threadIdx.x >> 5), per_row);
-  uint8_t q[kUnroll1], b[kUnroll1];
+__global__ void __launch_bounds__(kThreads) decode_any_kernel(const uint8_t* __restrict__ ck, ActLayout l, int64_t rows, uint32_t cols,
+                                                              T* __restrict__ x, int64_t ld, Step step) {
+  __shared__ __align__(16) uint8_t bufs[kWarps][1024];
+  const uint32_t per_row = (cols + 255) / 256, lane = threadIdx.x & 31;
+  const At first((int64_t)blockIdx.x * (kWarps * kUnroll) + (threadIdx.x >> 5), per_row);
+  uint2 q[kUnroll];
+  uint32_t b[kUnroll];
   At at = first;
 #pragma unroll
-  for (int u = 0; u < kUnroll1; ++u) {
-    if (at.row < rows) {
-      q[u] = ck[at.row * l.ld_q + at.item * kActBlock + lane];
-      b[u] = ck[l.e_off + at.row * l.ld_e + at.item];
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t c = at.item * 256 + lane * 8;
+    q[u] = make_uint2(0, 0);
+    b[u] = 0;
+    if (at.row < rows && c < l.ld_q) {
+      q[u] = __ldcs(reinterpret_cast<const uint2*>(ck + at.row * l.ld_q + c));
+      b[u] = ck[l.e_off + at.row * l.ld_e + c / kActBlock];
     }
     at.next(step, per_row);
   }
   at = first;
 #pragma unroll
-  for (int u = 0; u < kUnroll1; ++u) {
-    const uint32_t c = at.item * kActBlock + lane;
-    if (at.row < rows && c < cols) store1(x + at.row * ld + c, act_decode1(q[u], b[u]));
+  for (int u = 0; u < kUnroll; ++u) {
+    if (at.row < rows)                         // the same for the whole warp
+      store8_any(x + at.row * ld, act_values8(q[u], act_scale(b[u])), (int)at.item * 256, (int)cols, bufs[threadIdx.x >> 5]);
     at.next(step, per_row);
   }
 }
@@ -171,16 +157,13 @@ Step step_of(int64_t per_row, int64_t items) { return Step{(uint32_t)(items / pe
 template <typename T>
 int encode(const T* x, int64_t ld, int64_t rows, int64_t cols, uint8_t* ck, cudaStream_t s) {
   const ActLayout l = act_layout(rows, cols);
-  if (cols % 8 == 0 && rows_aligned(x, ld, sizeof(T))) {
-    const int64_t per_row = l.ld_q / 8;
-    const unsigned g = blocks_for(rows * per_row, kThreads * kUnroll);
-    return g ? launch_kernel(encode8_kernel<T>, g, kThreads, 0, s, 1, x, ld, rows, (uint32_t)cols, ck, l, step_of(per_row, kThreads))
-             : CZ_ERR_UNSUPPORTED;
-  }
-  const int64_t per_row = l.ld_q / kActBlock;
-  const unsigned g = blocks_for(rows * per_row, kWarps * kUnroll1);
-  return g ? launch_kernel(encode1_kernel<T>, g, kThreads, 0, s, 1, x, ld, rows, (uint32_t)cols, ck, l, step_of(per_row, kWarps))
-           : CZ_ERR_UNSUPPORTED;
+  const int64_t per_row = l.ld_q / 8;
+  const unsigned g = blocks_for(rows * per_row, kThreads * kUnroll);
+  if (g == 0) return CZ_ERR_UNSUPPORTED;
+  const Step step = step_of(per_row, kThreads);
+  if (cols % 8 == 0 && rows_aligned(x, ld, sizeof(T)))
+    return launch_kernel(encode8_kernel<T, true>, g, kThreads, 0, s, 1, x, ld, rows, (uint32_t)cols, ck, l, step);
+  return launch_kernel(encode8_kernel<T, false>, g, kThreads, 0, s, 1, x, ld, rows, (uint32_t)cols, ck, l, step);
 }
 
 // Columns of a checkpoint from `ck` on, which is moved to the first of them (a multiple of 32), laid out as l.
@@ -192,9 +175,9 @@ int decode(const uint8_t* ck, const ActLayout& l, int64_t rows, int64_t cols, T*
     return g ? launch_kernel(decode16_kernel<T>, g, kThreads, 0, s, 1, ck, l, rows, (uint32_t)cols, x, ld, step_of(per_row, kThreads))
              : CZ_ERR_UNSUPPORTED;
   }
-  const int64_t per_row = div_up(cols, kActBlock);
-  const unsigned g = blocks_for(rows * per_row, kWarps * kUnroll1);
-  return g ? launch_kernel(decode1_kernel<T>, g, kThreads, 0, s, 1, ck, l, rows, (uint32_t)cols, x, ld, step_of(per_row, kWarps))
+  const int64_t per_row = div_up(cols, 256);
+  const unsigned g = blocks_for(rows * per_row, kWarps * kUnroll);
+  return g ? launch_kernel(decode_any_kernel<T>, g, kThreads, 0, s, 1, ck, l, rows, (uint32_t)cols, x, ld, step_of(per_row, kWarps))
            : CZ_ERR_UNSUPPORTED;
 }
 

@@ -125,13 +125,6 @@ __device__ __forceinline__ uint32_t act_encode8(const F8& v, uint2* q) {
   return b;
 }
 
-// One element a lane, the warp's 32 lanes holding one block.  Every lane calls.
-__device__ __forceinline__ uint32_t act_encode1(float v, uint32_t* q) {
-  const uint32_t b = act_scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(v)));
-  *q = act_quantise(v, act_inv_scale(b), b);
-  return b;
-}
-
 // q + 128 as the low mantissa byte of 2^23: one difference gives q, one product x^ (both exact; integer
 // conversions run at an eighth of the rate).
 // s: 2^E, or 2^E times a factor, by which each value is then rounded once.
@@ -146,8 +139,6 @@ __device__ __forceinline__ F8 act_values8(uint2 q, float s) {
   }
   return v;
 }
-
-__device__ __forceinline__ float act_decode1(uint8_t q, uint32_t b) { return (float)(int8_t)q * act_scale(b); }
 
 #endif  // __CUDACC__
 

@@ -1,9 +1,8 @@
 // Device code shared by the forward and backward block norms.
 //
-// A row's elements are spread over `row_threads` threads, 8*C each.  VEC: element
-// (c, j) of thread t is column (c*row_threads + t)*8 + j, so that 8 elements move with
-// 16-byte accesses and 4 lanes hold one checkpoint block; otherwise column
-// (c*8 + j)*row_threads + t, one element a lane, a warp holding one block.
+// A row's elements are spread over `row_threads` threads n, 8*C each: element (c, j) of thread t is column
+// (c*n + t)*8 + j, so that 4 lanes hold one checkpoint block.  VEC: rows start on 16-byte boundaries and their length is
+// a multiple of 8; otherwise chunks come and go through the accesses for any alignment.
 #pragma once
 
 #include "act_ckpt.cuh"
@@ -12,10 +11,7 @@
 
 namespace cz {
 
-template <bool VEC>
-__device__ __forceinline__ int col_of(int c, int j, int t, int n) {
-  return VEC ? (c * n + t) * 8 + j : (c * 8 + j) * n + t;
-}
+__device__ __forceinline__ int col_of(int c, int j, int t, int n) { return (c * n + t) * 8 + j; }
 
 __device__ __forceinline__ float gate_value(float g, int act) {
   if (act == CZ_GATE_IDENTITY) return g;
@@ -41,75 +37,48 @@ __device__ __forceinline__ void gate_value_slope(float g, int act, float& value,
   }
 }
 
-// 8 elements of a chunk from a matrix row, zero past its end (VEC: as raw registers, the loads in flight).
+// 8 elements of a chunk from a matrix row, zero past its end, as raw registers (the loads in flight).
 template <typename T, bool VEC>
 struct Chunk;
 template <typename T>
 struct Chunk<T, true> {
   Raw8<T> r;
-  __device__ __forceinline__ void load(const T* row, int c, int t, int n, int cols) {
-    const int col = col_of<true>(c, 0, t, n);
-    if (col < cols) load8(row + col, r); else zero8(r);
+  __device__ __forceinline__ void load(const T* p, int64_t, const Extent&, int c, int t, int n, int cols) {
+    const int col = col_of(c, 0, t, n);
+    if (col < cols) load8(p + col, r); else zero8(r);
   }
-  __device__ __forceinline__ F8 get() const { return values(r); }
+  __device__ __forceinline__ F8 get(int, int, int, int) const { return values(r); }
 };
 template <typename T>
 struct Chunk<T, false> {
-  T r[8];
-  __device__ __forceinline__ void load(const T* row, int c, int t, int n, int cols) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<false>(c, j, t, n);
-      r[j] = T(0.f);
-      if (col < cols) r[j] = row[col];
-    }
+  RawAny<T> r;
+  __device__ __forceinline__ void load(const T* p, int64_t row, const Extent& x, int c, int t, int n, int cols) {
+    load8_any(r, p, row, x, col_of(c, 0, t, n), cols);
   }
-  __device__ __forceinline__ F8 get() const {
-    F8 v;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v.set(j, (float)r[j]);
-    return v;
-  }
+  __device__ __forceinline__ F8 get(int c, int t, int n, int cols) const { return values(raw8(r, col_of(c, 0, t, n), cols)); }
 };
 
+// A chunk to a row at p.  Every lane of the warp calls; buf: 1 KB of shared memory of the warp (not VEC).
 template <bool VEC, typename T>
-__device__ __forceinline__ void put(T* row, const F8& v, int c, int t, int n, int cols) {
+__device__ __forceinline__ void put(T* p, const F8& v, int c, int t, int n, int cols, uint8_t* buf) {
+  const int col = col_of(c, 0, t, n);
   if constexpr (VEC) {
-    const int col = col_of<true>(c, 0, t, n);
-    if (col < cols) store8(row + col, v);
+    if (col < cols) store8(p + col, v);
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<false>(c, j, t, n);
-      if (col < cols) store1(row + col, v.get(j));
-    }
+    const int first = col - 8 * (t & 31);
+    if (first < cols) store8_any(p, v, first, cols, buf);     // the same for the whole warp
   }
 }
 
-// Writes the chunk's part of a checkpoint row; every lane of the warp calls, `live` says
+// Writes the chunk's part of a checkpoint row (v: zero past cols); every lane of the warp calls, `live` says
 // whether the row exists.
-template <bool VEC>
-__device__ __forceinline__ void keep_chunk(uint8_t* ck, const ActLayout& l, int64_t row, bool live, const F8& v, int c,
-                                           int t, int n) {
-  if constexpr (VEC) {
-    uint2 q;
-    const uint32_t b = act_encode8(v, &q);
-    const int col = col_of<true>(c, 0, t, n);
-    if (live && col < l.ld_q) {
-      *reinterpret_cast<uint2*>(ck + row * l.ld_q + col) = q;
-      if ((t & 3) == 0) ck[l.e_off + row * l.ld_e + col / kActBlock] = (uint8_t)b;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t q;
-      const uint32_t b = act_encode1(v.get(j), &q);
-      const int col = col_of<false>(c, j, t, n);
-      if (live && col < l.ld_q) {
-        ck[row * l.ld_q + col] = (uint8_t)q;
-        if ((t & 31) == 0) ck[l.e_off + row * l.ld_e + col / kActBlock] = (uint8_t)b;
-      }
-    }
+__device__ __forceinline__ void keep_chunk(uint8_t* ck, const ActLayout& l, int64_t row, bool live, const F8& v, int c, int t, int n) {
+  uint2 q;
+  const uint32_t b = act_encode8(v, &q);
+  const int col = col_of(c, 0, t, n);
+  if (live && col < l.ld_q) {
+    *reinterpret_cast<uint2*>(ck + row * l.ld_q + col) = q;
+    if ((t & 3) == 0) ck[l.e_off + row * l.ld_e + col / kActBlock] = (uint8_t)b;
   }
 }
 
@@ -120,6 +89,19 @@ __device__ __forceinline__ int round4(int v) { return (v + 3) & ~3; }
 // own, so that lanes 8 columns apart read 16 bytes next to one another.
 __device__ __forceinline__ int plane_at(int col, int cols) {
   return (col & 4 ? round8(cols) >> 1 : 0) + ((col >> 3) << 2) + (col & 3);
+}
+
+// 8 elements of a vector over the columns in shared memory (zero from cols to the next multiple of 8).
+__device__ __forceinline__ F8 shared_vector(const float* w, int c, int t, int n, int cols) {
+  const int col = col_of(c, 0, t, n);
+  const float4 a = *reinterpret_cast<const float4*>(w + (col >> 1));
+  const float4 b = *reinterpret_cast<const float4*>(w + (col >> 1) + (round8(cols) >> 1));
+  F8 v;
+  v.p[0] = make_float2(a.x, a.y);
+  v.p[1] = make_float2(a.z, a.w);
+  v.p[2] = make_float2(b.x, b.y);
+  v.p[3] = make_float2(b.z, b.w);
+  return v;
 }
 
 }  // namespace cz

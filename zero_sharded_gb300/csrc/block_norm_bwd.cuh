@@ -36,7 +36,6 @@ struct Stage {
 struct BwdLayout {
   Stage at;
   int32_t stages;            // 0: rows are read from memory where they are used
-  int32_t row_bytes;         // bytes that arrive for a row
   int32_t vectors;           // floats of the vectors over the columns, which come first
   int32_t v_pre, v_post;     // w_pre, w_post; < 0: not there
   int32_t v_gate, v_slope;   // channel gate: y_scale act(gate), y_scale act'(gate) w_post
@@ -45,114 +44,79 @@ struct BwdLayout {
 // Bytes of a group's ring and its barriers.
 __host__ __device__ inline int round_ring(const BwdLayout& l) { return (l.stages * (l.at.bytes + 8) + 15) / 16 * 16; }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Where a row's copy starts in memory and how many bytes it takes: the row itself, or (any alignment) the vectors that
+// hold it, which lie inside the matrix except at its first and last row; those are not copied.
+struct Source {
+  const uint8_t* from;
+  uint32_t bytes;
+};
+template <typename T, bool VEC>
+__device__ __forceinline__ Source source_of(const void* base, int64_t row, const Extent& x, int cols) {
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(static_cast<const T*>(base) + row * x.ld);
+  if constexpr (VEC) return Source{p, (uint32_t)(cols * (int)sizeof(T))};
+  if (edge_row<T>(row, x)) return Source{nullptr, 0};
+  const uint32_t m = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+  return Source{p - m, (m + (uint32_t)(cols * (int)sizeof(T)) + 15) & ~15u};
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-// `bytes` bytes (a multiple of 16, 16-byte aligned) by the n threads of a row.
-__device__ __forceinline__ void copy_bytes16(uint32_t dst, const uint8_t* src, int bytes, int t, int n) {
-  for (int i = t * 16; i < bytes; i += n * 16) cp_async16(dst + i, src + i);
-}
-
-// One row of a rows x cols matrix.  Rows at any alignment are copied in 4-byte words: a bf16 row that starts in the
-// middle of a word takes its neighbour's half word along, except past either end of the matrix.
-template <typename T>
-__device__ __forceinline__ void copy_row(uint8_t* dst, const void* base, int64_t row, int64_t rows, int64_t ld, int cols, int t,
-                                         int n) {
-  const T* src = static_cast<const T*>(base) + row * ld;
-  const uint32_t to = smem_u32(dst);
-  if constexpr (sizeof(T) == 4) {
-    for (int i = t; i < cols; i += n) cp_async4(to + 4 * i, src + i, 4);
-  } else {
-    const int off = (int)(reinterpret_cast<uintptr_t>(src) & 2);
-    const uint8_t* word = reinterpret_cast<const uint8_t*>(src) - off;
-    const int words = (off + 2 * cols + 3) / 4;
-    for (int i = t; i < words; i += n) {
-      if (i == 0 && off && row == 0)        // nothing before the matrix is read
-        *reinterpret_cast<T*>(dst + 2) = *src;
-      else
-        cp_async4(to + 4 * i, word + 4 * i, (row == rows - 1 && 4 * i + 2 == off + 2 * cols) ? 2 : 4);
-    }
-  }
+__device__ __forceinline__ void copy_in(uint32_t to, const Source& s, uint64_t* bar) {
+  if (s.bytes) bulk_load(to, s.from, s.bytes, bar);
 }
 
-// The chunk's values of a row in shared memory (RING) or in memory.  VEC (here and below): the chunk is in the row.
+// The chunk's values of a row in shared memory (RING) or in memory; the chunk starts in the row.
 template <typename T, bool VEC, bool RING>
-__device__ __forceinline__ F8 take(const uint8_t* stage, const void* base, int64_t row, int64_t ld, int c, int t, int n, int cols) {
-  F8 v;
-  if constexpr (VEC) {
-    const int col = col_of<true>(c, 0, t, n);
+__device__ __forceinline__ F8 take(const uint8_t* stage, const void* base, int64_t row, const Extent& x, int c, int t, int n, int cols) {
+  const int col = col_of(c, 0, t, n);
+  const T* src = static_cast<const T*>(base) + row * x.ld;
+  if constexpr (RING && VEC) {
     Raw8<T> r;
-    if constexpr (RING) {
-      const uint4* s = reinterpret_cast<const uint4*>(stage + col * (int)sizeof(T));
-      r.a = s[0];
-      if constexpr (sizeof(T) == 4) r.b = s[1];
-    } else {
-      load8(static_cast<const T*>(base) + row * ld + col, r);
-    }
-    v = values(r);
+    const uint4* s = reinterpret_cast<const uint4*>(stage + col * (int)sizeof(T));
+    r.a = s[0];
+    if constexpr (sizeof(T) == 4) r.b = s[1];
+    return values(r);
   } else {
-    const T* src = static_cast<const T*>(base) + row * ld;
-    const T* s = RING ? reinterpret_cast<const T*>(stage + (sizeof(T) == 2 ? (reinterpret_cast<uintptr_t>(src) & 2) : 0)) : src;
+    Chunk<T, VEC> r;
+    if constexpr (RING) {
+      if (!edge_row<T>(row, x)) {
+        const uint4* s = reinterpret_cast<const uint4*>(stage + col * (int)sizeof(T));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<false>(c, j, t, n);
-      v.set(j, col < cols ? load1(s + col) : 0.f);
+        for (int i = 0; i < RawAny<T>::kVecs; ++i) {
+          const uint4 q = s[i];
+          r.r.w[4 * i] = q.x; r.r.w[4 * i + 1] = q.y; r.r.w[4 * i + 2] = q.z; r.r.w[4 * i + 3] = q.w;
+        }
+        r.r.from = (int)(reinterpret_cast<uintptr_t>(src) & 15);
+        return r.get(c, t, n, cols);
+      }
+      F8 v;                                    // a row that was not copied
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v.set(j, col + j < cols ? load1(src + col + j) : 0.f);
+      return v;
+    } else {
+      r.load(src, row, x, c, t, n, cols);
+      return r.get(c, t, n, cols);
     }
   }
-  return v;
 }
 
 // The chunk's values of a kept row times `factor`, each rounded once.
-template <bool VEC, bool RING>
+template <bool RING>
 __device__ __forceinline__ F8 take_kept(const uint8_t* q, const uint8_t* e, const uint8_t* ck, const ActLayout& l, int64_t row,
                                         float factor, int c, int t, int n) {
-  F8 v;
   if constexpr (!RING) {
     q = ck + row * l.ld_q;
     e = ck + l.e_off + row * l.ld_e;
   }
-  if constexpr (VEC) {
-    const int col = col_of<true>(c, 0, t, n);
-    v = act_values8(*reinterpret_cast<const uint2*>(q + col), act_scale(e[col / kActBlock]) * factor);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<false>(c, j, t, n);
-      v.set(j, col < l.ld_q ? act_decode1(q[col], e[col / kActBlock]) * factor : 0.f);
-    }
-  }
-  return v;
+  const int col = col_of(c, 0, t, n);
+  return act_values8(*reinterpret_cast<const uint2*>(q + col), act_scale(e[col / kActBlock]) * factor);
 }
 
 // 8 elements of a vector over the columns, in shared memory (RING) or memory.
-template <bool VEC, bool RING>
+template <bool RING>
 __device__ __forceinline__ F8 take_vector(const float* w, int c, int t, int n, int cols) {
+  if constexpr (RING) return shared_vector(w, c, t, n, cols);
+  const int col = col_of(c, 0, t, n);
   F8 v;
-  if constexpr (VEC) {
-    const int col = col_of<true>(c, 0, t, n);
-    if (RING || (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
-      const float* lo = RING ? w + (col >> 1) : w + col;
-      const float* hi = RING ? lo + (round8(cols) >> 1) : lo + 4;
-      const float4 a = *reinterpret_cast<const float4*>(lo), b = *reinterpret_cast<const float4*>(hi);
-      v.p[0] = make_float2(a.x, a.y);
-      v.p[1] = make_float2(a.z, a.w);
-      v.p[2] = make_float2(b.x, b.y);
-      v.p[3] = make_float2(b.z, b.w);
-    } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v.set(j, w[col + j]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<false>(c, j, t, n);
-      v.set(j, col < cols ? w[col] : 0.f);
-    }
-  }
+  for (int j = 0; j < 8; ++j) v.set(j, col + j < cols ? __ldg(w + col + j) : 0.f);
   return v;
 }
 
@@ -198,8 +162,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
                                                                            const __grid_constant__ BwdLayout lay) {
   __shared__ float red[2][64];
   extern __shared__ __align__(16) uint8_t dyn[];
-  constexpr bool BULK = RING && VEC;
-  const int n = !SOLO ? p.row_threads : VEC ? (int)blockDim.x : MAXT;   // fixed distances where elements move singly
+  const int n = SOLO ? (int)blockDim.x : p.row_threads;
   const int groups = SOLO ? 1 : p.rows_per_block;
   const int g = SOLO ? 0 : threadIdx.x / n, t = threadIdx.x - g * n, row_warps = n >> 5;
   const float inv_n = 1.f / (float)p.cols;
@@ -210,23 +173,26 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   const bool has_y = MODE || p.y;
   const int cols = p.cols;
   float* vec = reinterpret_cast<float*>(dyn);
+  // 1 KB a warp for stores at any alignment lies behind the rings
+  uint8_t* const buf = dyn + lay.vectors * 4 + groups * round_ring(lay) + (VEC ? 0 : (threadIdx.x >> 5) * 1024);
   uint8_t* ring = dyn + lay.vectors * 4 + g * round_ring(lay);
   // behind the stages a barrier each
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + lay.stages * lay.at.bytes);
   __shared__ float factors[SOLO ? 1 : 8][2][kFactors];
   if constexpr (RING) {
-    for (int i = threadIdx.x; i < cols; i += blockDim.x) {
-      const int at = VEC ? plane_at(i, cols) : i;
-      if (lay.v_pre >= 0) vec[lay.v_pre + at] = p.w_pre[i];
-      if (lay.v_post >= 0) vec[lay.v_post + at] = p.w_post[i];
+    for (int i = threadIdx.x; i < round8(cols); i += blockDim.x) {
+      const int at = plane_at(i, cols);
+      const bool is = i < cols;
+      if (lay.v_pre >= 0) vec[lay.v_pre + at] = is ? p.w_pre[i] : 0.f;
+      if (lay.v_post >= 0) vec[lay.v_post + at] = is ? p.w_post[i] : 0.f;
       if constexpr (CHANNEL) {
-        float value, slope;
-        gate_value_slope(static_cast<const float*>(p.gate)[i], p.gate_act, value, slope);
+        float value = 0.f, slope = 0.f;
+        if (is) gate_value_slope(static_cast<const float*>(p.gate)[i], p.gate_act, value, slope);
         vec[lay.v_gate + at] = p.y_scale * value;
-        vec[lay.v_slope + at] = p.y_scale * slope * (weighted ? p.w_post[i] : 1.f);
+        vec[lay.v_slope + at] = p.y_scale * slope * (is && weighted ? p.w_post[i] : 1.f);
       }
     }
-    if (VEC && t == 0) {
+    if (t == 0) {
       for (int i = 0; i < lay.stages; ++i) mbar_init(&full[i], 1);
       fence_barrier_init();
     }
@@ -236,71 +202,36 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   const int64_t row0 = (int64_t)blockIdx.x * groups + g;
   const int count = row0 < p.rows ? (int)((p.rows - row0 + stride - 1) / stride) : 0;   // rows of this group
 
-  // The copies of the group's i-th row into `stage`: aligned rows as whole copies by one thread (the warps take
-  // turns), which arrive on the stage's barrier; others in words by every thread.
+  // The copies of the group's i-th row into `stage`, which arrive on the stage's barrier; one thread issues them, the
+  // warps take turns.
   int turn = 0;
   auto issue = [&](int i, int stage) {
     if constexpr (RING) {
-      const int64_t row = row0 + i * stride;
-      uint8_t* st = ring + stage * lay.at.bytes;
-      if constexpr (VEC) {
-        const bool mine = t == 32 * turn;
-        if (++turn == row_warps) turn = 0;
-        if (mine && i < count) {
-          uint64_t* bar = &full[stage];
-          const uint32_t to = smem_u32(st);
-          mbar_arrive_expect_tx(bar, (uint32_t)lay.row_bytes);
-          if (pre) bulk_load(to + lay.at.dx, static_cast<const TY*>(p.dx) + row * p.ld_dx, cols * (int)sizeof(TY), bar);
-          if (has_dh_in) bulk_load(to + lay.at.dh, static_cast<const TH*>(p.dh_in) + row * p.ld_dh_in, cols * (int)sizeof(TH), bar);
-          if (pre) {
-            if (h_kept) {
-              bulk_load(to + lay.at.h, p.h_ckpt + row * p.ck.ld_q, (uint32_t)p.ck.ld_q, bar);
-              bulk_load(to + lay.at.h_e, p.h_ckpt + p.ck.e_off + row * p.ck.ld_e, (uint32_t)p.ck.ld_e, bar);
-            } else {
-              bulk_load(to + lay.at.h, static_cast<const TH*>(p.h) + row * p.ld_h, cols * (int)sizeof(TH), bar);
-            }
-          }
-          if (y_kept) {
-            bulk_load(to + lay.at.y, p.y_ckpt + row * p.ck.ld_q, (uint32_t)p.ck.ld_q, bar);
-            bulk_load(to + lay.at.y_e, p.y_ckpt + p.ck.e_off + row * p.ck.ld_e, (uint32_t)p.ck.ld_e, bar);
-          } else if (has_y) {
-            bulk_load(to + lay.at.y, static_cast<const TY*>(p.y) + row * p.ld_y, cols * (int)sizeof(TY), bar);
-          }
-          if (token) bulk_load(to + lay.at.gate, static_cast<const TY*>(p.gate) + row * p.ld_gate, cols * (int)sizeof(TY), bar);
-        }
-      } else {
-        if (i < count) {
-          if (p.pre) copy_row<TY>(st + lay.at.dx, p.dx, row, p.rows, p.ld_dx, cols, t, n);
-          if (p.dh_in) copy_row<TH>(st + lay.at.dh, p.dh_in, row, p.rows, p.ld_dh_in, cols, t, n);
-          if (p.pre) {
-            if (p.h_ckpt) {
-              copy_bytes16(smem_u32(st + lay.at.h), p.h_ckpt + row * p.ck.ld_q, (int)p.ck.ld_q, t, n);
-              copy_bytes16(smem_u32(st + lay.at.h_e), p.h_ckpt + p.ck.e_off + row * p.ck.ld_e, (int)p.ck.ld_e, t, n);
-            } else {
-              copy_row<TH>(st + lay.at.h, p.h, row, p.rows, p.ld_h, cols, t, n);
-            }
-          }
-          if (p.y_ckpt) {
-            copy_bytes16(smem_u32(st + lay.at.y), p.y_ckpt + row * p.ck.ld_q, (int)p.ck.ld_q, t, n);
-            copy_bytes16(smem_u32(st + lay.at.y_e), p.y_ckpt + p.ck.e_off + row * p.ck.ld_e, (int)p.ck.ld_e, t, n);
-          } else if (p.y) {
-            copy_row<TY>(st + lay.at.y, p.y, row, p.rows, p.ld_y, cols, t, n);
-          }
-          if (token) copy_row<TY>(st + lay.at.gate, p.gate, row, p.rows, p.ld_gate, cols, t, n);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      }
-    }
-  };
-  // Word copies: waits for this thread's part of the next row (a commit a row keeps the count), before a barrier.
-  auto arrived = [&]() {
-    if constexpr (RING && !VEC) {
-      switch (lay.stages) {
-        case 2: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 4: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        case 5: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+      const bool mine = t == 32 * turn;
+      if (++turn == row_warps) turn = 0;
+      if (mine && i < count) {
+        const int64_t row = row0 + i * stride;
+        const uint32_t to = smem_u32(ring) + stage * lay.at.bytes;
+        uint64_t* bar = &full[stage];
+        const Source none{nullptr, 0};
+        const Source s_dx = pre ? source_of<TY, VEC>(p.dx, row, Extent{p.rows, p.ld_dx}, cols) : none;
+        const Source s_dh = has_dh_in ? source_of<TH, VEC>(p.dh_in, row, Extent{p.rows, p.ld_dh_in}, cols) : none;
+        const Source s_h = !pre ? none
+                           : h_kept ? Source{p.h_ckpt + row * p.ck.ld_q, (uint32_t)p.ck.ld_q}
+                                    : source_of<TH, VEC>(p.h, row, Extent{p.rows, p.ld_h}, cols);
+        const Source s_y = y_kept ? Source{p.y_ckpt + row * p.ck.ld_q, (uint32_t)p.ck.ld_q}
+                           : has_y ? source_of<TY, VEC>(p.y, row, Extent{p.rows, p.ld_y}, cols) : none;
+        const Source s_g = token ? source_of<TY, VEC>(p.gate, row, Extent{p.rows, p.ld_gate}, cols) : none;
+        const uint32_t e = (uint32_t)p.ck.ld_e;
+        mbar_arrive_expect_tx(bar, s_dx.bytes + s_dh.bytes + s_h.bytes + s_y.bytes + s_g.bytes + (pre && h_kept ? e : 0) +
+                                       (y_kept ? e : 0));
+        copy_in(to + lay.at.dx, s_dx, bar);
+        copy_in(to + lay.at.dh, s_dh, bar);
+        copy_in(to + lay.at.h, s_h, bar);
+        if (pre && h_kept) bulk_load(to + lay.at.h_e, p.h_ckpt + p.ck.e_off + row * p.ck.ld_e, e, bar);
+        copy_in(to + lay.at.y, s_y, bar);
+        if (y_kept) bulk_load(to + lay.at.y_e, p.y_ckpt + p.ck.e_off + row * p.ck.ld_e, e, bar);
+        copy_in(to + lay.at.gate, s_g, bar);
       }
     }
   };
@@ -308,7 +239,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   F8 a_post[C], a_pre[C], a_gate[C];
   F8 d[C], hv[C], yv[C];                     // of the row under way
   F8 dl[C], yl[C];                           // w_post dn and y^ of the row before, whose dy is not written yet
-  bool in[C];                                // aligned rows: a chunk is in the row or not
+  bool in[C];                                // whether a chunk starts in the row
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     a_post[c].fill(0.f);
@@ -317,16 +248,11 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
     d[c].fill(0.f);
     hv[c].fill(0.f);
     yv[c].fill(0.f);
-    in[c] = !VEC || col_of<VEC>(c, 0, t, n) < cols;
+    in[c] = col_of(c, 0, t, n) < cols;
   }
   float sum2 = 0.f, r_last = 0.f;
 
   for (int i = 0; i < lay.stages; ++i) issue(i, i);
-  if constexpr (RING && !VEC) {
-    // the first row has to be there; from then on a row's copies are waited for before the barrier of the row before
-    arrived();
-    group_sync(g, n);
-  }
   int stage = 0;
   uint32_t phase = 0;
   bool there = true;
@@ -354,26 +280,29 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
       r_pre = factors[g][0][f];
       r_post = factors[g][1][f];
       // a copy that never arrives shows as NaN in the row and in the column sums
-      there = there && (!BULK || mbar_poll(&full[stage], phase, nullptr, nullptr, kTimeoutClocks));
+      there = there && (!RING || mbar_poll(&full[stage], phase, nullptr, nullptr, kTimeoutClocks));
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (!in[c]) continue;
-        if (has_dh_in) d[c] = take<TH, VEC, RING>(st + lay.at.dh, p.dh_in, row, p.ld_dh_in, c, t, n, cols);
+        if (!in[c]) {
+          d[c].fill(0.f);
+          continue;
+        }
+        if (has_dh_in) d[c] = take<TH, VEC, RING>(st + lay.at.dh, p.dh_in, row, Extent{p.rows, p.ld_dh_in}, c, t, n, cols);
         else d[c].fill(0.f);
         if (!there) d[c].fill(__uint_as_float(0x7FC00000u));
         if (pre) {
           if (h_kept) {
-            hv[c] = take_kept<VEC, RING>(st + lay.at.h, st + lay.at.h_e, p.h_ckpt, p.ck, row, r_pre, c, t, n);
+            hv[c] = take_kept<RING>(st + lay.at.h, st + lay.at.h_e, p.h_ckpt, p.ck, row, r_pre, c, t, n);
           } else {
-            hv[c] = take<TH, VEC, RING>(st + lay.at.h, p.h, row, p.ld_h, c, t, n, cols);
+            hv[c] = take<TH, VEC, RING>(st + lay.at.h, p.h, row, Extent{p.rows, p.ld_h}, c, t, n, cols);
 #pragma unroll
             for (int j = 0; j < 4; ++j) hv[c].p[j] = mul2(hv[c].p[j], both(r_pre));
           }
-          F8 dx = take<TY, VEC, RING>(st + lay.at.dx, p.dx, row, p.ld_dx, c, t, n, cols);
+          F8 dx = take<TY, VEC, RING>(st + lay.at.dx, p.dx, row, Extent{p.rows, p.ld_dx}, c, t, n, cols);
 #pragma unroll
           for (int j = 0; j < 4; ++j) a_pre[c].p[j] = fma2(dx.p[j], hv[c].p[j], a_pre[c].p[j]);
           if (w_pre) {
-            const F8 w = take_vector<VEC, RING>(RING ? vec + lay.v_pre : p.w_pre, c, t, n, cols);
+            const F8 w = take_vector<RING>(RING ? vec + lay.v_pre : p.w_pre, c, t, n, cols);
 #pragma unroll
             for (int j = 0; j < 4; ++j) dx.p[j] = mul2(dx.p[j], w.p[j]);
           }
@@ -386,18 +315,17 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
           sum1 += part.x + part.y;
         }
         if (y_kept) {
-          yv[c] = take_kept<VEC, RING>(st + lay.at.y, st + lay.at.y_e, p.y_ckpt, p.ck, row, post ? r_post : 1.f, c, t, n);
+          yv[c] = take_kept<RING>(st + lay.at.y, st + lay.at.y_e, p.y_ckpt, p.ck, row, post ? r_post : 1.f, c, t, n);
         } else if (has_y) {
-          yv[c] = take<TY, VEC, RING>(st + lay.at.y, p.y, row, p.ld_y, c, t, n, cols);
+          yv[c] = take<TY, VEC, RING>(st + lay.at.y, p.y, row, Extent{p.rows, p.ld_y}, c, t, n, cols);
           if (post)
 #pragma unroll
             for (int j = 0; j < 4; ++j) yv[c].p[j] = mul2(yv[c].p[j], both(r_post));
         }
-        if (token) gv[c] = take<TY, VEC, RING>(st + lay.at.gate, p.gate, row, p.ld_gate, c, t, n, cols);
+        if (token) gv[c] = take<TY, VEC, RING>(st + lay.at.gate, p.gate, row, Extent{p.rows, p.ld_gate}, c, t, n, cols);
       }
     }
-    // behind this barrier every thread has read this row, and (word copies) the next row's are there
-    arrived();
+    // behind this barrier every thread has read this row
     const float2 sums = group_sum(make_float2(sum1, sum2), red[i & 1], g, n, row_warps);
     issue(i + lay.stages, stage);
     if (RING && ++stage == lay.stages) {
@@ -408,11 +336,11 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
       const float2 k = both(-sums.y * inv_n), r = both(r_last);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (!in[c]) continue;
+        if (VEC && !in[c]) continue;           // (any alignment: the warp stores together)
         if (post)
 #pragma unroll
           for (int j = 0; j < 4; ++j) dl[c].p[j] = mul2(r, fma2(k, yl[c].p[j], dl[c].p[j]));
-        put<VEC>(out_y, dl[c], c, t, n, cols);
+        put<VEC>(out_y, dl[c], c, t, n, cols, buf);
       }
     }
     if (!live) break;
@@ -421,7 +349,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
     r_last = r_post;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (!in[c]) continue;
+      if (VEC && !in[c]) continue;
       F8 o;
       if (pre)
 #pragma unroll
@@ -429,17 +357,23 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
       if (has_dh) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) o.p[j] = mul2(both(p.h_scale), d[c].p[j]);
-        put<VEC>(out_h, o, c, t, n, cols);
+        put<VEC>(out_h, o, c, t, n, cols, buf);
       }
       F8 w;
-      if (weighted) w = take_vector<VEC, RING>(RING ? vec + lay.v_post : p.w_post, c, t, n, cols);
+      if (weighted && in[c]) w = take_vector<RING>(RING ? vec + lay.v_post : p.w_post, c, t, n, cols);
+      else w.fill(0.f);
       if (CHANNEL || token) {
         F8 value, slope;
         if constexpr (CHANNEL && RING) {
-          value = take_vector<VEC, true>(vec + lay.v_gate, c, t, n, cols);
-          slope = take_vector<VEC, true>(vec + lay.v_slope, c, t, n, cols);
+          value.fill(0.f);
+          slope.fill(0.f);
+          if (in[c]) {
+            value = take_vector<true>(vec + lay.v_gate, c, t, n, cols);
+            slope = take_vector<true>(vec + lay.v_slope, c, t, n, cols);
+          }
         } else {
-          if constexpr (CHANNEL) gv[c] = take_vector<VEC, false>(static_cast<const float*>(p.gate), c, t, n, cols);
+          if constexpr (CHANNEL) gv[c] = take_vector<false>(static_cast<const float*>(p.gate), c, t, n, cols);
+          else if (!in[c]) gv[c].fill(0.f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             float v, sl;
@@ -455,7 +389,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
           else o.p[j] = mul2(slope.p[j], yd);
           d[c].p[j] = mul2(value.p[j], d[c].p[j]);
         }
-        if (!CHANNEL && p.dgate) put<VEC>(static_cast<TY*>(p.dgate) + row * p.ld_dgate, o, c, t, n, cols);
+        if (!CHANNEL && p.dgate) put<VEC>(static_cast<TY*>(p.dgate) + row * p.ld_dgate, o, c, t, n, cols, buf);
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[c].p[j] = mul2(both(p.y_scale), d[c].p[j]);
@@ -476,7 +410,6 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   }
 
   if (!p.partial) return;
-  if constexpr (RING && !VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
   // the block's column sums: the row groups are added in order
   float* out = p.partial + (int64_t)blockIdx.x * 3 * cols;
   float* fold = reinterpret_cast<float*>(dyn);
@@ -488,7 +421,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
       for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int col = col_of<VEC>(c, j, t, n);
+          const int col = col_of(c, j, t, n);
           if (col < cols) fold[g * round4(cols) + col] = (v == 0 ? a_post[c] : v == 1 ? a_pre[c] : a_gate[c]).get(j);
         }
       __syncthreads();
@@ -500,7 +433,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
     } else {
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        put<VEC>(out + v * cols, v == 0 ? a_post[c] : v == 1 ? a_pre[c] : a_gate[c], c, t, n, cols);
+        put<VEC>(out + v * cols, v == 0 ? a_post[c] : v == 1 ? a_pre[c] : a_gate[c], c, t, n, cols, buf);
     }
   }
 }
@@ -523,10 +456,8 @@ BwdLayout layout_of(const NormParams& p, int h_bytes, int y_bytes, int64_t room)
   int64_t off = 0;
   auto slot = [&](bool on, int64_t bytes) {
     const int64_t was = off;
-    if (on) {
-      off += round_up(bytes + 4, 16);         // a word more for rows that start inside one
-      l.row_bytes += (int32_t)bytes;
-    }
+    if (on)
+      off += round_up(bytes, 32) + 32;        // rows that start inside a vector, and whole chunks past a row's end
     return (int32_t)was;
   };
   l.at.dx = slot(p.pre, (int64_t)p.cols * y_bytes);
@@ -547,13 +478,13 @@ template <typename TH, typename TY, bool VEC, bool CHANNEL, int MODE>
 int launch_ring(NormParams p, const BwdLayout& l, int blocks, cudaStream_t s) {
   const bool solo = p.rows_per_block == 1;
   const int64_t fold = solo ? 0 : (int64_t)sizeof(float) * p.rows_per_block * round_up(p.cols, 4);
-  const int64_t smem = std::max<int64_t>(fold, l.vectors * 4 + (int64_t)round_ring(l) * p.rows_per_block);
+  const int64_t smem = std::max<int64_t>(fold, l.vectors * 4 + (int64_t)round_ring(l) * p.rows_per_block +
+                                                   (VEC ? 0 : p.row_threads * p.rows_per_block / 32 * 1024));
   const int most = p.row_threads <= 256 ? 256 : p.row_threads <= 640 ? 640 : 1024;
   auto* k = !solo ? norm_bwd_kernel<TH, TY, VEC, 1, 256, false, true, CHANNEL, MODE>
             : most == 256 ? norm_bwd_kernel<TH, TY, VEC, 1, 256, true, true, CHANNEL, MODE>
             : most == 640 ? norm_bwd_kernel<TH, TY, VEC, 1, 640, true, true, CHANNEL, MODE>
                           : norm_bwd_kernel<TH, TY, VEC, 1, 1024, true, true, CHANNEL, MODE>;
-  if (solo && !VEC) p.row_threads = most;
   const int threads = p.row_threads * p.rows_per_block;
   if (blocks_per_sm(reinterpret_cast<const void*>(k), threads, (int)smem) < 1) return CZ_ERR_CUDA;
   return launch_kernel(k, dim3((unsigned)blocks), dim3((unsigned)threads), (size_t)smem, s, 1, p, l);
@@ -561,12 +492,13 @@ int launch_ring(NormParams p, const BwdLayout& l, int blocks, cudaStream_t s) {
 
 template <typename TH, typename TY, bool VEC, bool CHANNEL>
 int launch_c(NormParams p, int blocks, cudaStream_t s) {
-  const BwdLayout l = layout_of(p, sizeof(TH), sizeof(TY), norm_bwd_room(p));
+  const BwdLayout l = layout_of(p, sizeof(TH), sizeof(TY),
+                                norm_bwd_room(p) - (VEC ? 0 : p.row_threads * p.rows_per_block / 32 * 1024));
   if (l.stages == 0 || p.cols > 8 * 1024) {   // rows too wide: 16 elements a thread, straight from memory
     BwdLayout none{};
-    p.row_threads = VEC ? (int32_t)round_up(div_up(p.cols, 16), 32) : 1024;
+    p.row_threads = (int32_t)round_up(div_up(p.cols, 16), 32);
     return launch_kernel(norm_bwd_kernel<TH, TY, VEC, 2, 1024, true, false, CHANNEL, kAny>, dim3((unsigned)blocks),
-                         dim3((unsigned)p.row_threads), 0, s, 1, p, none);
+                         dim3((unsigned)p.row_threads), VEC ? 0 : p.row_threads / 32 * 1024, s, 1, p, none);
   }
   // the tests that kTensors and kKept save are worth their kernels for aligned bf16 activations
   if constexpr (VEC && sizeof(TY) == 2) {

@@ -18,31 +18,10 @@
 namespace cz {
 namespace {
 
-// A vector over the columns in shared memory (aligned rows: two planes), or ones.
+// The vectors over the columns in shared memory.
 struct FwdVectors {
   int32_t post, pre, gate, floats;   // offsets in floats; < 0: not there
 };
-
-template <bool VEC>
-__device__ __forceinline__ F8 shared_vector(const float* w, int c, int t, int n, int cols) {
-  F8 v;
-  if constexpr (VEC) {
-    const int col = col_of<true>(c, 0, t, n);
-    const float4 a = *reinterpret_cast<const float4*>(w + (col >> 1));
-    const float4 b = *reinterpret_cast<const float4*>(w + (col >> 1) + (round8(cols) >> 1));
-    v.p[0] = make_float2(a.x, a.y);
-    v.p[1] = make_float2(a.z, a.w);
-    v.p[2] = make_float2(b.x, b.y);
-    v.p[3] = make_float2(b.z, b.w);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<false>(c, j, t, n);
-      v.set(j, col < cols ? w[col] : 0.f);
-    }
-  }
-  return v;
-}
 
 // Sum of v over the threads of a row; `red` holds a float for every warp of the block, and consecutive sums alternate
 // between two such arrays (one barrier a sum).
@@ -60,29 +39,29 @@ __device__ __forceinline__ float row_sum(float v, float* red, int row_warps) {
   return v;
 }
 
-// SOLO: a row a block.  FULL: both norms with weights, h' and x wanted, of the checkpoints at most x's.  Rows at any
-// alignment (no VEC) move element by element; with MAXT threads, known when compiling, the
-// elements of a thread lie at fixed distances (16 in place of 96 instructions an element).
+// SOLO: a row a block.  FULL: both norms with weights, h' and x wanted, of the checkpoints at most x's.
 template <typename TH, typename TY, bool VEC, int C, int MAXT, int MINB, bool SOLO, bool FULL>
 __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const __grid_constant__ NormParams p, const FwdVectors at) {
   __shared__ float red[2][32];
   extern __shared__ __align__(16) float vec[];
-  const int n = !SOLO ? p.row_threads : VEC ? (int)blockDim.x : MAXT;
+  const int n = SOLO ? (int)blockDim.x : p.row_threads;
   const int g = SOLO ? 0 : threadIdx.x / n, t = threadIdx.x - g * n, row_warps = n >> 5;
   const int groups = SOLO ? 1 : p.rows_per_block;
   const int cols = p.cols;
   const float inv_n = 1.f / (float)cols;
   const bool post = FULL || p.post, pre = FULL || p.pre, w_post = FULL || at.post >= 0, w_pre = FULL || at.pre >= 0;
-  for (int i = threadIdx.x; i < cols; i += blockDim.x) {
-    const int to = VEC ? plane_at(i, cols) : i;
-    if (at.post >= 0) vec[at.post + to] = p.w_post[i];
-    if (at.pre >= 0) vec[at.pre + to] = p.w_pre[i];
-    if (at.gate >= 0) vec[at.gate + to] = gate_value(static_cast<const float*>(p.gate)[i], p.gate_act);
+  for (int i = threadIdx.x; i < round8(cols); i += blockDim.x) {
+    const int to = plane_at(i, cols);
+    const bool is = i < cols;
+    if (at.post >= 0) vec[at.post + to] = is ? p.w_post[i] : 0.f;
+    if (at.pre >= 0) vec[at.pre + to] = is ? p.w_pre[i] : 0.f;
+    if (at.gate >= 0) vec[at.gate + to] = is ? gate_value(static_cast<const float*>(p.gate)[i], p.gate_act) : 0.f;
   }
+  uint8_t* const buf = reinterpret_cast<uint8_t*>(vec + at.floats) + (VEC ? 0 : (threadIdx.x >> 5) * 1024);
   __syncthreads();
   bool in[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) in[c] = !VEC || col_of<VEC>(c, 0, t, n) < cols;
+  for (int c = 0; c < C; ++c) in[c] = col_of(c, 0, t, n) < cols;
   const bool token = p.gate_kind == kGateToken;
 
   Chunk<TY, VEC> ry[C], rg[C];
@@ -94,19 +73,19 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const __grid_const
   const TY* gate = token ? static_cast<const TY*>(p.gate) + row * p.ld_gate : nullptr;
   TH* h_out = static_cast<TH*>(p.h_out) + row * p.ld_h_out;
   TY* x = static_cast<TY*>(p.x) + row * p.ld_x;
-  auto fetch = [&](bool live) {
-    const int in_row = live ? cols : 0;
+  auto fetch = [&](int64_t row) {
+    const int in_row = row < p.rows ? cols : 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      ry[c].load(y, c, t, n, in_row);
-      rh[c].load(h_in, c, t, n, in_row);
-      if (token) rg[c].load(gate, c, t, n, in_row);
+      ry[c].load(y, row, Extent{p.rows, p.ld_y}, c, t, n, in_row);
+      rh[c].load(h_in, row, Extent{p.rows, p.ld_h}, c, t, n, in_row);
+      if (token) rg[c].load(gate, row, Extent{p.rows, p.ld_gate}, c, t, n, in_row);
     }
     y += stride * p.ld_y;
     h_in += stride * p.ld_h;
     if (token) gate += stride * p.ld_gate;
   };
-  fetch(row < p.rows);
+  fetch(row);
   for (int64_t base = (int64_t)blockIdx.x * groups; base < p.rows;
        base += stride, row += stride, h_out += stride * p.ld_h_out, x += stride * p.ld_x) {
     const bool live = SOLO || row < p.rows;
@@ -115,12 +94,12 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const __grid_const
     float s = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      v[c] = ry[c].get();
+      v[c] = ry[c].get(c, t, n, cols);
       float2 part = mul2(v[c].p[0], v[c].p[0]);
 #pragma unroll
       for (int j = 1; j < 4; ++j) part = fma2(v[c].p[j], v[c].p[j], part);
       s += part.x + part.y;
-      if (!FULL && p.y_ckpt) keep_chunk<VEC>(p.y_ckpt, p.ck, row, live, v[c], c, t, n);
+      if (!FULL && p.y_ckpt) keep_chunk(p.y_ckpt, p.ck, row, live, v[c], c, t, n);
     }
     float r_post = 1.f;
     if (post) {
@@ -131,21 +110,21 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const __grid_const
     const float k = p.y_scale * r_post;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      h[c] = rh[c].get();
+      h[c] = rh[c].get(c, t, n, cols);
       if (in[c]) {
         if (w_post) {
-          const F8 w = shared_vector<VEC>(vec + at.post, c, t, n, cols);
+          const F8 w = shared_vector(vec + at.post, c, t, n, cols);
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[c].p[j] = mul2(v[c].p[j], w.p[j]);
         }
         if (p.gate_kind != kGateNone) {
           F8 w;
           if (token) {
-            w = rg[c].get();
+            w = rg[c].get(c, t, n, cols);
 #pragma unroll
             for (int j = 0; j < 8; ++j) w.set(j, gate_value(w.get(j), p.gate_act));
           } else {
-            w = shared_vector<VEC>(vec + at.gate, c, t, n, cols);
+            w = shared_vector(vec + at.gate, c, t, n, cols);
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[c].p[j] = mul2(v[c].p[j], w.p[j]);
@@ -159,11 +138,11 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const __grid_const
       }
       s += part.x + part.y;
     }
-    fetch(row + stride < p.rows);              // in flight until the next turn
+    fetch(row + stride);                       // in flight until the next turn
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (FULL || p.h_out) put<VEC>(h_out, h[c], c, t, n, in_row);
-      if (!FULL && p.h_ckpt) keep_chunk<VEC>(p.h_ckpt, p.ck, row, live, h[c], c, t, n);
+      if (FULL || p.h_out) put<VEC>(h_out, h[c], c, t, n, in_row, buf);
+      if (!FULL && p.h_ckpt) keep_chunk(p.h_ckpt, p.ck, row, live, h[c], c, t, n);
     }
     if (!pre) {
       if (post && row_warps > 1) __syncthreads();     // red[0] is read before the next row writes it
@@ -174,32 +153,29 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const __grid_const
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       if (w_pre && in[c]) {
-        const F8 w = shared_vector<VEC>(vec + at.pre, c, t, n, cols);
+        const F8 w = shared_vector(vec + at.pre, c, t, n, cols);
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[c].p[j] = mul2(h[c].p[j], w.p[j]);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) h[c].p[j] = mul2(h[c].p[j], both(r_pre));
-      if (FULL || p.x) put<VEC>(x, h[c], c, t, n, in_row);
-      if (p.x_ckpt) keep_chunk<VEC>(p.x_ckpt, p.ck, row, live, h[c], c, t, n);
+      if (FULL || p.x) put<VEC>(x, h[c], c, t, n, in_row, buf);
+      if (p.x_ckpt) keep_chunk(p.x_ckpt, p.ck, row, live, h[c], c, t, n);
     }
     if (!post && row_warps > 1) __syncthreads();      // likewise red[1]
   }
 }
 
 template <typename TH, typename TY, bool VEC, bool FULL>
-int launch_f(NormParams p, const FwdVectors& at, cudaStream_t s) {
-  const bool solo = p.rows_per_block == 1;
-  const int per_thread = p.row_threads * 8 >= p.cols ? 1 : 2;
-  // two chunks a thread from 2048 columns on; registers for 3 x 256, 2 x 320 or one larger block an SM
-  const int most = !solo || per_thread == 1 ? 256 : p.row_threads <= 320 ? 320 : p.row_threads <= 512 ? 512 : 1024;
-  auto* k = !solo ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, false, FULL>
-            : per_thread == 1 ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, true, FULL>
-            : most == 320 ? norm_fwd_kernel<TH, TY, VEC, 2, 320, 2, true, FULL>
-            : most == 512 ? norm_fwd_kernel<TH, TY, VEC, 2, 512, 1, true, FULL>
-                          : norm_fwd_kernel<TH, TY, VEC, 2, 1024, 1, true, FULL>;
-  if (solo && !VEC) p.row_threads = most;
-  const int threads = p.row_threads * p.rows_per_block, smem = at.floats * 4;
+int launch_f(const NormParams& p, const FwdVectors& at, cudaStream_t s) {
+  // Registers for 3 x 256, 2 x 320 or one larger block an SM.
+  auto* k = p.rows_per_block > 1 ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, false, FULL>
+            : p.row_threads <= 256 && p.row_threads * 8 >= p.cols ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, true, FULL>
+            : p.row_threads * 8 >= p.cols ? norm_fwd_kernel<TH, TY, VEC, 1, 640, 1, true, FULL>
+            : p.row_threads <= 320 ? norm_fwd_kernel<TH, TY, VEC, 2, 320, 2, true, FULL>
+            : p.row_threads <= 512 ? norm_fwd_kernel<TH, TY, VEC, 2, 512, 1, true, FULL>
+                                   : norm_fwd_kernel<TH, TY, VEC, 2, 1024, 1, true, FULL>;
+  const int threads = p.row_threads * p.rows_per_block, smem = at.floats * 4 + (VEC ? 0 : threads / 32 * 1024);
   const int per_sm = blocks_per_sm(reinterpret_cast<const void*>(k), threads, smem);
   if (per_sm < 1) return CZ_ERR_CUDA;
   const int64_t blocks = std::min<int64_t>(div_up(p.rows, p.rows_per_block), (int64_t)per_sm * sm_count());
@@ -217,7 +193,7 @@ int launch_c(const NormParams& p, cudaStream_t s) {
   at.post = vector(p.post && p.w_post);
   at.pre = vector(p.pre && p.w_pre);
   at.gate = vector(p.gate_kind == kGateChannel);
-  if constexpr (VEC && sizeof(TY) == 2)
+  if constexpr (sizeof(TY) == 2)
     if (at.post >= 0 && at.pre >= 0 && p.h_out && p.x && !p.h_ckpt && !p.y_ckpt) return launch_f<TH, TY, VEC, true>(p, at, s);
   return launch_f<TH, TY, VEC, false>(p, at, s);
 }

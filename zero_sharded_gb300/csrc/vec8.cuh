@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "ptx.cuh"
 
@@ -129,5 +130,123 @@ __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+
+// ---- rows at any alignment: a thread still holds 8 consecutive elements
+//
+// A load takes the aligned vectors that hold them (the neighbour's is in the first-level cache) and shifts.  A store
+// goes through 1 KB of shared memory a warp, from which lanes write consecutive words.
+
+// A matrix, so far as these accesses need to know it.
+struct Extent {
+  int64_t rows, ld;
+};
+
+// Words first .. first + N - 1 + (shift16 ? half a word : 0) of w, `first` 0 to 3.
+template <int N, int M>
+__device__ __forceinline__ void window(const uint32_t (&w)[M], int first, uint32_t shift_bits, uint32_t (&r)[N]) {
+  static_assert(M >= N + 4, "words");
+  uint32_t u[N + 3], t[N + 1];
+#pragma unroll
+  for (int i = 0; i < N + 3; ++i) u[i] = (first & 1) ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < N + 1; ++i) t[i] = (first & 2) ? u[i + 2] : u[i];
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = __funnelshift_r(t[i], t[i + 1], shift_bits);
+}
+
+// The vectors that hold 8 elements, and where these start in them: shifted when they are used, so that the loads
+// stay in flight.
+template <typename T>
+struct RawAny {
+  static constexpr int kVecs = 8 * sizeof(T) / 16 + 1;
+  alignas(16) uint32_t w[4 * kVecs];
+  int from;                                // byte of the first vector
+};
+
+// Whether a row's vectors may reach past the matrix (or over more than the next row): its elements are read one by one.
+template <typename T>
+__device__ __forceinline__ bool edge_row(int64_t row, const Extent& x) {
+  return row == 0 || row + 1 == x.rows || x.ld * (int64_t)sizeof(T) < 16;
+}
+
+// Elements col .. col + 7 of row `row` at p.  Only vectors inside the matrix are read.
+template <typename T>
+__device__ __forceinline__ void load8_any(RawAny<T>& r, const T* p, int64_t row, const Extent& x, int col, int cols) {
+#pragma unroll
+  for (int i = 0; i < 4 * RawAny<T>::kVecs; ++i) r.w[i] = 0;
+  r.from = 0;
+  if (col >= cols) return;
+  if (edge_row<T>(row, x)) {
+    alignas(16) T e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = col + j < cols ? p[col + j] : T(0.f);
+    memcpy(r.w, e, sizeof(e));
+    return;
+  }
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p + col);
+  const uint4* v = reinterpret_cast<const uint4*>(a & ~(uintptr_t)15);
+  r.from = (int)(a & 15);
+  const int need = min(8, cols - col) * (int)sizeof(T) + r.from;   // bytes from the first vector's start
+#pragma unroll
+  for (int i = 0; i < RawAny<T>::kVecs; ++i) {
+    if (need > 16 * i) {
+      const uint4 q = v[i];
+      r.w[4 * i] = q.x; r.w[4 * i + 1] = q.y; r.w[4 * i + 2] = q.z; r.w[4 * i + 3] = q.w;
+    }
+  }
+}
+
+// The 8 elements, zero from cols on.
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const RawAny<T>& r, int col, int cols) {
+  alignas(16) uint32_t o[2 * sizeof(T)];
+  window(r.w, r.from >> 2, 8 * (r.from & 3), o);
+  if (col + 8 > cols) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j >= cols) {
+        if constexpr (sizeof(T) == 2) o[j / 2] &= (j & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+        else o[j] = 0;
+      }
+  }
+  Raw8<T> v;
+  memcpy(&v, o, sizeof(o));
+  return v;
+}
+
+// The warp's 256 consecutive elements from column `first` on (lane L holds 8 from first + 8 L) to a row at p, up to
+// cols.  buf: 1 KB of shared memory of this warp.  Every lane calls.
+__device__ __forceinline__ void store8_any(float* p, const F8& v, int first, int cols, void* buf) {
+  const int lane = threadIdx.x & 31, n = min(256, cols - first);
+  float4* s = static_cast<float4*>(buf) + 2 * lane;
+  s[0] = make_float4(v.p[0].x, v.p[0].y, v.p[1].x, v.p[1].y);
+  s[1] = make_float4(v.p[2].x, v.p[2].y, v.p[3].x, v.p[3].y);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = 32 * i + lane;
+    if (e < n) p[first + e] = static_cast<const float*>(buf)[e];
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void store8_any(__nv_bfloat16* p, const F8& v, int first, int cols, void* buf) {
+  const int lane = threadIdx.x & 31, n = min(256, cols - first);
+  static_cast<uint4*>(buf)[lane] = pack(v);
+  __syncwarp();
+  uint16_t* to = reinterpret_cast<uint16_t*>(p + first);
+  const int off = (int)(reinterpret_cast<uintptr_t>(to) >> 1) & 1;   // 1: elements 2 w - 1, 2 w share a word
+  const uint32_t* s = static_cast<const uint32_t*>(buf);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int w = 32 * i + lane, e = 2 * w - off;
+    uint32_t x = s[w];
+    if (off) x = (x << 16) | (w > 0 ? s[w - 1] >> 16 : 0);
+    if (e >= 0 && e + 1 < n) *reinterpret_cast<uint32_t*>(to + e) = x;
+    else if (e < 0 && n > 0) to[0] = (uint16_t)(x >> 16);
+    else if (e < n) to[e] = (uint16_t)x;
+  }
+  if (off && n == 256 && lane == 31) to[255] = (uint16_t)(s[127] >> 16);
+  __syncwarp();
+}
 
 }  // namespace cz
