@@ -53,15 +53,13 @@ bool opt_matrix_ok(const void* p, const cz_norm_args& a, int64_t ld, int64_t byt
   return p == nullptr || matrix_ok(p, a.rows, a.cols, ld, bytes);
 }
 
-NormParams params_of(const cz_norm_args& a, bool backward, bool vec) {
+NormParams params_of(const cz_norm_args& a, bool backward) {
   NormParams p{};
   p.rows = a.rows;
   p.cols = (int32_t)a.cols;
   // The backward holds eight fp32 values an element in registers: 8 elements a thread as long as a row
-  // fits 1024 threads.  The forward holds four, and 16 a thread halve what a row costs every thread, but
-  // rows at any alignment take twice the registers for their loads.
-  const int64_t eights = backward ? 1024 : vec ? 256 : 640;
-  const int64_t per = a.cols <= 8 * eights ? 8 : 16;
+  // fits 1024 threads.  The forward holds four, and 16 a thread halve what a row costs every thread.
+  const int64_t per = a.cols <= 8 * (backward ? 1024 : 256) ? 8 : 16;
   p.row_threads = (int32_t)round_up(div_up(a.cols, per), 32);
   p.rows_per_block = std::max(1, 256 / p.row_threads);   // narrow rows share a block of up to 8 warps
   p.post = a.post_norm;
@@ -128,7 +126,7 @@ extern "C" int cz_block_norm_fwd(const cz_norm_args* args, void* stream) {
   const bool vec = a.cols % 8 == 0 && rows_aligned(a.h, a.ld_h, hb) && rows_aligned(a.y, a.ld_y, yb) &&
                    rows_aligned(a.h_out, a.ld_h_out, hb) && rows_aligned(a.x, a.ld_x, yb) &&
                    (a.gate_kind != CZ_GATE_TOKEN || rows_aligned(a.gate, a.ld_gate, yb));
-  NormParams p = params_of(a, false, vec);
+  NormParams p = params_of(a, false);
   p.h_out = a.h_out;
   p.x = a.x;
   p.ld_h_out = a.ld_h_out;
@@ -184,7 +182,7 @@ extern "C" int cz_block_norm_bwd(const cz_norm_args* args, void* stream) {
                    rows_aligned(a.dh_in, a.ld_dh_in, hb) && rows_aligned(a.dh, a.ld_dh, hb) &&
                    rows_aligned(a.dy, a.ld_dy, yb) &&
                    (!token || (rows_aligned(a.gate, a.ld_gate, yb) && rows_aligned(a.dgate, a.ld_dgate, yb)));
-  NormParams p = params_of(a, true, vec);
+  NormParams p = params_of(a, true);
   p.dx = a.dx;
   p.dh_in = a.dh_in;
   p.dh = a.dh;

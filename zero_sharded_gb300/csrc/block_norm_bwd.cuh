@@ -480,9 +480,10 @@ int launch_ring(NormParams p, const BwdLayout& l, int blocks, cudaStream_t s) {
   const int64_t fold = solo ? 0 : (int64_t)sizeof(float) * p.rows_per_block * round_up(p.cols, 4);
   const int64_t smem = std::max<int64_t>(fold, l.vectors * 4 + (int64_t)round_ring(l) * p.rows_per_block +
                                                    (VEC ? 0 : p.row_threads * p.rows_per_block / 32 * 1024));
-  const int most = p.row_threads <= 256 ? 256 : p.row_threads <= 640 ? 640 : 1024;
+  const int most = p.row_threads <= 256 ? 256 : p.row_threads <= 512 ? 512 : p.row_threads <= 640 ? 640 : 1024;
   auto* k = !solo ? norm_bwd_kernel<TH, TY, VEC, 1, 256, false, true, CHANNEL, MODE>
             : most == 256 ? norm_bwd_kernel<TH, TY, VEC, 1, 256, true, true, CHANNEL, MODE>
+            : most == 512 ? norm_bwd_kernel<TH, TY, VEC, 1, 512, true, true, CHANNEL, MODE>
             : most == 640 ? norm_bwd_kernel<TH, TY, VEC, 1, 640, true, true, CHANNEL, MODE>
                           : norm_bwd_kernel<TH, TY, VEC, 1, 1024, true, true, CHANNEL, MODE>;
   const int threads = p.row_threads * p.rows_per_block;

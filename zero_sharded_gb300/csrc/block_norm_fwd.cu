@@ -168,11 +168,11 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const __grid_const
 
 template <typename TH, typename TY, bool VEC, bool FULL>
 int launch_f(const NormParams& p, const FwdVectors& at, cudaStream_t s) {
-  // Registers for 3 x 256, 2 x 320 or one larger block an SM.
+  // Registers for 3 x 256, 2 x 320 or one larger block an SM; loads at any alignment take more of them.
   auto* k = p.rows_per_block > 1 ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, false, FULL>
-            : p.row_threads <= 256 && p.row_threads * 8 >= p.cols ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, true, FULL>
-            : p.row_threads * 8 >= p.cols ? norm_fwd_kernel<TH, TY, VEC, 1, 640, 1, true, FULL>
-            : p.row_threads <= 320 ? norm_fwd_kernel<TH, TY, VEC, 2, 320, 2, true, FULL>
+            : p.row_threads * 8 >= p.cols ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, true, FULL>
+            : !VEC && p.row_threads <= 256 ? norm_fwd_kernel<TH, TY, VEC, 2, 256, 2, true, FULL>
+            : p.row_threads <= 320 ? norm_fwd_kernel<TH, TY, VEC, 2, 320, VEC ? 2 : 1, true, FULL>
             : p.row_threads <= 512 ? norm_fwd_kernel<TH, TY, VEC, 2, 512, 1, true, FULL>
                                    : norm_fwd_kernel<TH, TY, VEC, 2, 1024, 1, true, FULL>;
   const int threads = p.row_threads * p.rows_per_block, smem = at.floats * 4 + (VEC ? 0 : threads / 32 * 1024);

@@ -222,10 +222,13 @@ __device__ __forceinline__ void store8_any(float* p, const F8& v, int first, int
   s[0] = make_float4(v.p[0].x, v.p[0].y, v.p[1].x, v.p[1].y);
   s[1] = make_float4(v.p[2].x, v.p[2].y, v.p[3].x, v.p[3].y);
   __syncwarp();
+  float* to = p + first + lane;
+  const float* from = static_cast<const float*>(buf) + lane;
+  if (n == 256) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = 32 * i + lane;
-    if (e < n) p[first + e] = static_cast<const float*>(buf)[e];
+    for (int i = 0; i < 8; ++i) to[32 * i] = from[32 * i];
+  } else {
+    for (int i = lane; i < n; i += 32, to += 32, from += 32) *to = *from;
   }
   __syncwarp();
 }
@@ -235,17 +238,23 @@ __device__ __forceinline__ void store8_any(__nv_bfloat16* p, const F8& v, int fi
   __syncwarp();
   uint16_t* to = reinterpret_cast<uint16_t*>(p + first);
   const int off = (int)(reinterpret_cast<uintptr_t>(to) >> 1) & 1;   // 1: elements 2 w - 1, 2 w share a word
-  const uint32_t* s = static_cast<const uint32_t*>(buf);
+  if (n < 256) {                           // the row's end: element by element
+    for (int e = lane; e < n; e += 32) to[e] = static_cast<const uint16_t*>(buf)[e];
+  } else if (off) {
+    uint32_t* words = reinterpret_cast<uint32_t*>(to + 2 * lane - 1);
+    const uint32_t* s = static_cast<const uint32_t*>(buf) + lane;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int w = 32 * i + lane, e = 2 * w - off;
-    uint32_t x = s[w];
-    if (off) x = (x << 16) | (w > 0 ? s[w - 1] >> 16 : 0);
-    if (e >= 0 && e + 1 < n) *reinterpret_cast<uint32_t*>(to + e) = x;
-    else if (e < 0 && n > 0) to[0] = (uint16_t)(x >> 16);
-    else if (e < n) to[e] = (uint16_t)x;
+    for (int i = 0; i < 4; ++i) {
+      if (i == 0 && lane == 0) to[0] = (uint16_t)s[0];
+      else words[32 * i] = __funnelshift_r(s[32 * i - 1], s[32 * i], 16);
+    }
+    if (lane == 31) to[255] = (uint16_t)(s[96] >> 16);
+  } else {
+    uint32_t* words = reinterpret_cast<uint32_t*>(to) + lane;
+    const uint32_t* s = static_cast<const uint32_t*>(buf) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) words[32 * i] = s[32 * i];
   }
-  if (off && n == 256 && lane == 31) to[255] = (uint16_t)(s[127] >> 16);
   __syncwarp();
 }
 
