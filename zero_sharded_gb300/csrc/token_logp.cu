@@ -4,14 +4,13 @@
 //   s = sum 2^d_j,  w = sum 2^d_j d_j,  lse = m inv_temp + ln s,  entropy = ln s - ln2 w / s
 // in one pass over the row: every thread keeps (m, s, w) of the elements it has seen and
 // rescales s and w when the maximum of the next vectors exceeds m; the threads', warps' and cluster blocks'
-// triples are joined in a fixed order.  x - m is formed before the scale, so that rows of a
-// type's lowest value and masked -inf entries stay finite; x is held to >= m - 150 / c, where 2^d
+// triples are joined in a fixed order.  x is held to >= m - 150 / c, where 2^d
 // is 0, so that a masked entry's 2^d d is 0 and not NaN.  Maxima of bf16 are taken before unpacking and
 // the rest runs on pairs: five instructions an element, where memory leaves time for eight.
 //
-// Top alternatives cost no second pass: the k-th largest of the maxima of groups of 4
+// Top alternatives cost no second pass: the k-th largest of the maxima of groups of 4 to 16
 // threads (disjoint parts of the row) is a bound that the k largest elements reach, so only the parts of threads
-// whose own maximum reaches it are read again, each by a whole warp.  Keys of (value,
+// whose own maximum reaches it are read again, by the whole block at once.  Keys of (value,
 // complement of the index) make the order total.  Should ties or a skewed row
 // put forward more than the buffer holds, k rounds of a block-wide maximum below the last
 // key find them instead.
@@ -29,7 +28,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroups = kThreads / 4;     // groups of 4 threads
+constexpr int kGroups = kThreads / 4;     // groups of 4 threads (of 8 or 16 for few alternatives)
 static_assert(kGroups == 64, "two groups a lane");
 constexpr int kCand = 1024;               // candidates that the buffer holds
 constexpr float kMasked = -1e37f;         // a largest logit below this: -inf or a type's lowest value throughout
@@ -169,7 +168,8 @@ struct LogpShared {
   float group[kGroups];
   Sums warp[kWarps];
   Sums all;
-  int n_cand;
+  uint16_t part[kThreads];
+  int n_cand, n_part;
 };
 
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
@@ -180,23 +180,24 @@ template <typename T>
 __device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool singles, float own_max, int k) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float g = own_max;
-#pragma unroll
-  for (int d = 1; d < 4; d <<= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, d));
-  if ((lane & 3) == 0) sh.group[warp * 8 + (lane >> 2)] = g;
-  if (threadIdx.x == 0) sh.n_cand = 0;
+  const int width = k <= 8 ? 16 : k <= 16 ? 8 : 4, groups = kThreads / width;   // twice as many groups as k at least
+  for (int d = 1; d < width; d <<= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, d));
+  if ((lane & (width - 1)) == 0) sh.group[threadIdx.x / width] = g;
+  if (threadIdx.x == 0) sh.n_cand = sh.n_part = 0;
   if ((int)threadIdx.x < k) sh.top[threadIdx.x] = 0;
   __syncthreads();
   // the k-th largest group maximum (every warp for itself)
-  const float ga = sh.group[lane], gb = sh.group[lane + 32];
+  const float ga = lane < groups ? sh.group[lane] : -INFINITY, gb = lane + 32 < groups ? sh.group[lane + 32] : -INFINITY;
   int ra = 0, rb = 0;
 #pragma unroll 8
-  for (int i = 0; i < kGroups; ++i) {
+  for (int i = 0; i < groups; ++i) {
     const float o = sh.group[i];
     ra += (o > ga || (o == ga && i < lane)) ? 1 : 0;
     rb += (o > gb || (o == gb && i < lane + 32)) ? 1 : 0;
   }
   const bool nan = __any_sync(0xffffffffu, ga != ga || gb != gb);
-  const uint32_t ha = __ballot_sync(0xffffffffu, ra == k - 1), hb = __ballot_sync(0xffffffffu, rb == k - 1);
+  const uint32_t ha = __ballot_sync(0xffffffffu, ra == k - 1 && lane < groups),
+                 hb = __ballot_sync(0xffffffffu, rb == k - 1 && lane + 32 < groups);
   const float bound = ha ? __shfl_sync(0xffffffffu, ga, __ffs(ha) - 1) : __shfl_sync(0xffffffffu, gb, max(__ffs(hb) - 1, 0));
   if (!nan) {
     auto put_forward = [&](float x, uint32_t i) {
@@ -205,13 +206,26 @@ __device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool 
         if (at < kCand) sh.cand[at] = key_of(x, i);
       }
     };
-    for (uint32_t todo = __ballot_sync(0xffffffffu, own_max >= bound); todo; todo &= todo - 1) {
-      const int first = v0 + warp * 32 + __ffs(todo) - 1;
-      for (int i = first + lane * kThreads; i < v1; i += 32 * kThreads) {
-        float v[Vec<T>::N];
-        Vec<T>::values(__ldg(reinterpret_cast<const uint4*>(r.p + r.head) + i), v);
+    // the parts that reach the bound, read again by the whole block: one trip to memory for all
+    if (own_max >= bound) sh.part[atomicAdd(&sh.n_part, 1)] = (uint16_t)threadIdx.x;
+    __syncthreads();
+    const int per = (v1 - v0 + kThreads - 1) / kThreads, total = sh.n_part * per;
+    for (int i0 = threadIdx.x; i0 < total; i0 += 2 * kThreads) {
+      uint4 raw[2];
+      int at[2];
 #pragma unroll
-        for (int j = 0; j < Vec<T>::N; ++j) put_forward(v[j], (uint32_t)(r.head + i * Vec<T>::N + j));
+      for (int u = 0; u < 2; ++u) {
+        const int i = i0 + u * kThreads, part = i / per;
+        at[u] = i < total ? v0 + sh.part[part] + (i - part * per) * kThreads : v1;
+        if (at[u] < v1) raw[u] = __ldg(reinterpret_cast<const uint4*>(r.p + r.head) + at[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (at[u] >= v1 || !(Vec<T>::largest(raw[u]) >= bound)) continue;
+        float v[Vec<T>::N];
+        Vec<T>::values(raw[u], v);
+#pragma unroll
+        for (int j = 0; j < Vec<T>::N; ++j) put_forward(v[j], (uint32_t)(r.head + at[u] * Vec<T>::N + j));
       }
     }
     if (singles && (int)threadIdx.x < r.singles()) {
@@ -281,13 +295,28 @@ __global__ void __launch_bounds__(kThreads, 4) logp_fwd_kernel(const __grid_cons
   const uint4* body = reinterpret_cast<const uint4*>(r.p + r.head);
   const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;          // -inf
   float2 s2[2] = {both(0.f), both(0.f)}, w2[2] = {both(0.f), both(0.f)};     // the sums, in four parts
-  float2 base2 = both(0.f);                                                  // minus the maximum
+  // 2^(x c - base) with base = rint(max c): one fused operation an element.  Past |base| = 2^20 its
+  // rounding would show, and x - max is formed first.
+  float base = 0.f;
+  bool large = false;
   typename Vec<T>::Floor low = Vec<T>::floor_of(-150.f / c);
   uint4 next[U];
   auto fetch = [&](int i) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
       next[u] = i + u * kThreads < v1 ? ld_stream16(body + i + u * kThreads) : make_uint4(none, none, none, none);
+  };
+  auto add = [&](const uint4& raw, auto is_large) {
+    float v[N];
+    Vec<T>::values(Vec<T>::hold(raw, low), v);
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      const float2 x = make_float2(v[j], v[j + 1]);
+      const float2 d = is_large() ? mul2(add2(x, both(-a.m)), both(c)) : fma2(x, both(c), both(-base));
+      const float2 e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+      s2[(j >> 1) & 1] = add2(s2[(j >> 1) & 1], e);
+      w2[(j >> 1) & 1] = fma2(e, d, w2[(j >> 1) & 1]);
+    }
   };
   fetch(v0 + (int)threadIdx.x);
   for (int i = v0 + (int)threadIdx.x; i < v1; i += U * kThreads) {
@@ -296,30 +325,41 @@ __global__ void __launch_bounds__(kThreads, 4) logp_fwd_kernel(const __grid_cons
     for (int u = 0; u < U; ++u) raw[u] = next[u];
     if (i + U * kThreads < v1) fetch(i + U * kThreads);
     const float m = Vec<T>::largest(Vec<T>::larger(Vec<T>::larger(raw[0], raw[1]), Vec<T>::larger(raw[2], raw[3])));
-    if (!(m <= a.m)) {                         // grown (or NaN): bring the sums to the new maximum
+    if (!(m <= a.m)) {                         // grown (or NaN): bring the sums to the new base
       const float nm = max_nan(m, a.m);
-      const float d = fmaxf((a.m - nm) * c, -150.f), f = exp2_fast(d);
+      const bool was_large = large;
+      large = !(fabsf(nm * c) < 1048576.f);
+      const float new_base = large ? 0.f : rintf(nm * c);
+      // how much further the old sums lie below the new base
+      float d = large || was_large ? (a.m - nm) * c : base - new_base;
+      if (large && !was_large) d += base - a.m * c;
+      if (was_large && !large) d += nm * c - new_base;
+      d = fmaxf(d, -150.f);
+      const float f = a.m == -INFINITY ? 0.f : exp2_fast(d);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         w2[q] = mul2(both(f), fma2(s2[q], both(d), w2[q]));
         s2[q] = mul2(both(f), s2[q]);
       }
       a.m = nm;
-      base2 = both(-nm);
+      base = new_base;
       // 2^-7 |m| further down, so that rounding to T never lifts it to the maximum
       low = Vec<T>::floor_of(fmaxf(nm - fmaf(fabsf(nm), 0.0078125f, 150.f / c), Vec<T>::kLowest));
     }
+    if (!large) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float v[N];
-      Vec<T>::values(Vec<T>::hold(raw[u], low), v);
+      for (int u = 0; u < U; ++u) add(raw[u], [] { return false; });
+    } else {
 #pragma unroll
-      for (int j = 0; j < N; j += 2) {
-        const float2 d = mul2(add2(make_float2(v[j], v[j + 1]), base2), both(c));
-        const float2 e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
-        s2[(j >> 1) & 1] = add2(s2[(j >> 1) & 1], e);
-        w2[(j >> 1) & 1] = fma2(e, d, w2[(j >> 1) & 1]);
-      }
+      for (int u = 0; u < U; ++u) add(raw[u], [] { return true; });
+    }
+  }
+  if (!large && a.m != -INFINITY) {            // from the base to the maximum itself
+    const float d = fmaf(-a.m, c, base), f = exp2_fast(d);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      w2[q] = mul2(both(f), fma2(s2[q], both(d), w2[q]));
+      s2[q] = mul2(both(f), s2[q]);
     }
   }
   const float2 st = add2(s2[0], s2[1]), wt = add2(w2[0], w2[1]);
