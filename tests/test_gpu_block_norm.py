@@ -164,6 +164,19 @@ def test_backward(rows, cols, ht, yt, gate, act, pad, norms, ckpt):
     _backward(_inputs(rows, cols, ht, yt, gate, pad, seed=cols + 1), rows, cols, act, *norms, ckpt)
 
 
+@pytest.mark.parametrize("rows,cols,ht,yt,gate,act,pad,ckpt", [
+    (170300, 8, "bf16", "bf16", "channel", "sigmoid", 0, False),          # 70 rows a row group
+    (400, 8456, "bf16", "bf16", "channel", "silu", 0, False),             # rows over the blocks of a cluster, several rows each
+    (400, 8456, "f32", "bf16", "channel", "silu", 0, True), (311, 8193, "bf16", "bf16", None, "identity", 1, False),
+    (170, 12299, "f32", "f32", "token", "sigmoid", 0, False), (170, 16384, "f32", "f32", "token", "silu", 0, False),
+    (165, 16383, "bf16", "bf16", None, "identity", 0, True)])
+def test_backward_walks_over_rows(rows, cols, ht, yt, gate, act, pad, ckpt):
+    s = _inputs(rows, cols, ht, yt, gate, pad, seed=cols + 2)
+    a = _backward(s, rows, cols, act, True, True, ckpt)
+    b = _backward(s, rows, cols, act, True, True, ckpt)
+    assert all(torch.equal(a[k], b[k]) for k in a)
+
+
 def test_backward_accumulates_and_repeats_bit_for_bit():
     s = _inputs(1500, 320, "f32", "bf16", "channel", 0, seed=5)
     _backward(s, 1500, 320, "sigmoid", True, True, False, accumulate=True)

@@ -226,6 +226,32 @@ int blocks_per_sm(const void* kernel, int threads, int smem) {
   return n;
 }
 
+int clusters_at_once(const void* kernel, int threads, int smem, int cluster) {
+  struct Known {
+    const void* kernel;
+    int dev, threads, smem, cluster, clusters;
+  };
+  static thread_local Known known[16] = {};
+  int dev = 0;
+  if (note_cuda_error(cudaGetDevice(&dev)) != cudaSuccess) return 0;
+  Known& k = known[((reinterpret_cast<uintptr_t>(kernel) >> 4) + (uintptr_t)threads + (uintptr_t)smem / 16 + (uintptr_t)cluster) % 16];
+  if (k.kernel == kernel && k.dev == dev && k.threads == threads && k.smem == smem && k.cluster == cluster) return k.clusters;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sm_count() / cluster * cluster));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (note_cuda_error(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return 0;
+  k = Known{kernel, dev, threads, smem, cluster, n};
+  return n;
+}
+
 int sm_count() {
   static thread_local int known_dev = -1, known = 1;
   int dev = 0;

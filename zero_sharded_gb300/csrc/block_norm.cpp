@@ -57,9 +57,9 @@ NormParams params_of(const cz_norm_args& a, bool backward) {
   NormParams p{};
   p.rows = a.rows;
   p.cols = (int32_t)a.cols;
-  // The backward holds eight fp32 values an element in registers: 8 elements a thread as long as a row
-  // fits 1024 threads.  The forward holds four, and 16 a thread halve what a row costs every thread.
-  const int64_t per = a.cols <= 8 * (backward ? 1024 : 256) ? 8 : 16;
+  // The backward holds eight fp32 values an element in registers: 8 elements a thread.  The forward holds four, and 16
+  // a thread halve what a row costs every thread.
+  const int64_t per = backward || a.cols <= 8 * 256 ? 8 : 16;
   p.row_threads = (int32_t)round_up(div_up(a.cols, per), 32);
   p.rows_per_block = std::max(1, 256 / p.row_threads);   // narrow rows share a block of up to 8 warps
   p.post = a.post_norm;
@@ -194,11 +194,15 @@ extern "C" int cz_block_norm_bwd(const cz_norm_args* args, void* stream) {
   p.ld_dy = a.ld_dy;
   p.ld_dgate = a.ld_dgate;
   p.partial = sums ? static_cast<float*>(a.workspace) : nullptr;
-  const int blocks = (int)std::min<int64_t>(div_up(a.rows, p.rows_per_block), std::min(kMaxBlocks, norm_bwd_blocks_per_sm(p) * sm_count()));
-  if (blocks > 0) {
-    const int r = launch_norm_bwd(p, a.h_dtype == CZ_F32, a.y_dtype == CZ_F32, vec, blocks, stream);
+  const bool h_f32 = a.h_dtype == CZ_F32, y_f32 = a.y_dtype == CZ_F32;
+  BwdLayout l{};
+  int units = 0;
+  if (a.rows > 0) {
+    units = std::min(kMaxBlocks, plan_norm_bwd(p, h_f32, y_f32, vec, l));
+    if (units < 1) return CZ_ERR_UNSUPPORTED;
+    const int r = launch_norm_bwd(p, l, h_f32, y_f32, vec, units, stream);
     if (r != CZ_OK) return r;
   }
   if (!sums) return CZ_OK;
-  return launch_norm_fold(p.partial, blocks, p.cols, a.dw_post, a.dw_pre, dgate, a.accumulate, stream);
+  return launch_norm_fold(p.partial, units, p.cols, a.dw_post, a.dw_pre, dgate, a.accumulate, stream);
 }

@@ -3,8 +3,8 @@
 
 namespace cz {
 
-int launch_norm_bwd_f32(const NormParams& p, bool y_f32, bool vec, int blocks, void* stream) {
-  return launch_y<float, false>(p, y_f32, vec, blocks, stream);
+int launch_norm_bwd_f32(const NormParams& p, const BwdLayout& l, bool y_f32, bool vec, int& units, void* stream) {
+  return launch_y<float, false>(p, l, y_f32, vec, units, stream);
 }
 
 }  // namespace cz

@@ -72,5 +72,7 @@ int launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, 
 // Prepares `kernel` for `smem` bytes of dynamic shared memory and says how many of its blocks an SM holds (0: it
 // cannot run).  Both are asked of the driver once for each kernel, size and device, not on every call.
 int blocks_per_sm(const void* kernel, int threads, int smem);
+// Clusters of `cluster` such blocks that the GPU holds at once (a GPC's SMs need not divide by their size); 0: none.
+int clusters_at_once(const void* kernel, int threads, int smem, int cluster);
 
 }  // namespace cz
