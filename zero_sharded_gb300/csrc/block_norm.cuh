@@ -13,9 +13,17 @@ namespace cz {
 
 __device__ __forceinline__ int col_of(int c, int j, int t, int n) { return (c * n + t) * 8 + j; }
 
+// s = sigmoid(g) and less = sigmoid(-g) from one exponential and one reciprocal, neither with cancellation.  The approximate division is within 2 units of the last place, the exponential's error is larger.
+__device__ __forceinline__ void sigmoid_both(float g, float& s, float& less) {
+  const float e = __expf(-fabsf(g)), big = __fdividef(1.f, 1.f + e), small = e * big;
+  s = g < 0.f ? small : big;
+  less = g < 0.f ? big : small;
+}
+
 __device__ __forceinline__ float gate_value(float g, int act) {
   if (act == CZ_GATE_IDENTITY) return g;
-  const float s = 1.f / (1.f + __expf(-g));
+  float s, less;
+  sigmoid_both(g, s, less);
   return act == CZ_GATE_SIGMOID ? s : g * s;
 }
 
@@ -26,14 +34,14 @@ __device__ __forceinline__ void gate_value_slope(float g, int act, float& value,
     slope = 1.f;
     return;
   }
-  const float s = 1.f / (1.f + __expf(-g));
-  const float one_less = 1.f / (1.f + __expf(g));   // 1 - s without cancellation
+  float s, less;
+  sigmoid_both(g, s, less);
   if (act == CZ_GATE_SIGMOID) {
     value = s;
-    slope = s * one_less;
+    slope = s * less;
   } else {
     value = g * s;
-    slope = s * (1.f + g * one_less);
+    slope = s * (1.f + g * less);
   }
 }
 
