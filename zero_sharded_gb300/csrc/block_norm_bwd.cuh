@@ -14,8 +14,8 @@
 // SM has 2300 clocks for a row of 5120 columns at the memory's rate, and as many instructions as that allows.  The
 // groups' column sums are added in a fixed order by a second kernel, so results do not depend on timing.  Rows that
 // no block holds are spread over a cluster.  Measured: 16384 x 5120 from checkpoints, channel gate, 186 us
-// (floor 124; the rest is arithmetic and the barrier's latency); 8192 x 7168 bf16 142 (104).  Rows at any alignment are
-// shifted into place on top: 4099 x 2047, fp32 stream, token gate 82 (27).
+// (floor 124; the rest is arithmetic and the barrier's latency); 8192 x 7168 bf16 135 (104).  Rows at any alignment are
+// shifted into place on top: 4099 x 2047, fp32 stream, token gate 67 (27).
 //
 // Compiled once for each type of the residual stream, with and without a channel gate.
 #pragma once
@@ -41,10 +41,10 @@ struct Source {
   uint32_t bytes;
 };
 template <typename T, bool VEC>
-__device__ __forceinline__ Source source_of(const void* base, int64_t row, const Extent& x, int cols) {
-  const uint8_t* p = reinterpret_cast<const uint8_t*>(static_cast<const T*>(base) + row * x.ld);
+__device__ __forceinline__ Source source_of(const T* base, int64_t row, int64_t ld, bool edge, int cols) {
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(base + row * ld);
   if constexpr (VEC) return Source{p, (uint32_t)(cols * (int)sizeof(T))};
-  if (edge_row<T>(row, x)) return Source{nullptr, 0};
+  if (edge) return Source{nullptr, 0};
   const uint32_t m = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
   return Source{p - m, (m + (uint32_t)(cols * (int)sizeof(T)) + 15) & ~15u};
 }
@@ -54,7 +54,7 @@ __device__ __forceinline__ void copy_in(uint32_t to, const Source& s, uint64_t* 
 
 // The chunk's values of a row in its stage; the chunk starts in the row.
 template <typename T, bool VEC>
-__device__ __forceinline__ F8 take(const uint8_t* stage, const void* base, int64_t row, const Extent& x, int c, int t, int n, int cols) {
+__device__ __forceinline__ F8 take(const uint8_t* stage, const T* base, int64_t row, int64_t ld, bool edge, int c, int t, int n, int cols) {
   const int col = col_of(c, 0, t, n);
   const uint4* s = reinterpret_cast<const uint4*>(stage + col * (int)sizeof(T));
   if constexpr (VEC) {
@@ -63,17 +63,18 @@ __device__ __forceinline__ F8 take(const uint8_t* stage, const void* base, int64
     if constexpr (sizeof(T) == 4) r.b = s[1];
     return values(r);
   } else {
-    const T* src = static_cast<const T*>(base) + row * x.ld;
-    if (!edge_row<T>(row, x)) {
+    if (!edge) {
       Chunk<T, false> r;
 #pragma unroll
       for (int i = 0; i < RawAny<T>::kVecs; ++i) {
         const uint4 q = s[i];
         r.r.w[4 * i] = q.x; r.r.w[4 * i + 1] = q.y; r.r.w[4 * i + 2] = q.z; r.r.w[4 * i + 3] = q.w;
       }
-      r.r.from = (int)(reinterpret_cast<uintptr_t>(src) & 15);
+      // the row's offset from a 16-byte boundary: its address modulo 2^32 tells
+      r.r.from = (int)(((uint32_t)reinterpret_cast<uintptr_t>(base) + (uint32_t)row * ((uint32_t)ld * (uint32_t)sizeof(T))) & 15u);
       return r.get(c, t, n, cols);
     }
+    const T* src = base + row * ld;
     F8 v;                                      // a row that was not copied
 #pragma unroll
     for (int j = 0; j < 8; ++j) v.set(j, col + j < cols ? load1(src + col + j) : 0.f);
@@ -217,6 +218,8 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   const int64_t row0 = (int64_t)unit * groups + g;
   const int count = row0 < p.rows ? (int)((p.rows - row0 + stride - 1) / stride) : 0;   // rows of this group
 
+  // Whether a row's vectors may reach past the matrix (or over more than the next row): it is read element by element.
+  auto edge_of = [&](int64_t row) { return !VEC && (row == 0 || row + 1 == p.rows || p.cols < 8); };
   // The copies of the group's i-th row into `stage`, which arrive on the stage's barrier; one thread issues them, the
   // warps take turns.
   int turn = 0;
@@ -225,18 +228,19 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
     if (++turn == row_warps) turn = 0;
     if (mine && i < count) {
       const int64_t row = row0 + i * stride;
+      const bool edge = edge_of(row);
       const uint32_t to = smem_u32(ring) + stage * lay.at.bytes;
       uint64_t* bar = &full[stage];
       const Source none{nullptr, 0};
       const uint32_t q_bytes = SPLIT ? (uint32_t)min(p.width, (int)p.ck.ld_q - c0) : (uint32_t)p.ck.ld_q;
-      const Source s_dx = pre ? source_of<TY, VEC>(p_dx, row, Extent{p.rows, p.ld_dx}, cols) : none;
-      const Source s_dh = has_dh_in ? source_of<TH, VEC>(p_dh, row, Extent{p.rows, p.ld_dh_in}, cols) : none;
+      const Source s_dx = pre ? source_of<TY, VEC>(p_dx, row, p.ld_dx, edge, cols) : none;
+      const Source s_dh = has_dh_in ? source_of<TH, VEC>(p_dh, row, p.ld_dh_in, edge, cols) : none;
       const Source s_h = !pre ? none
                          : h_kept ? Source{p.h_ckpt + row * p.ck.ld_q + c0, q_bytes}
-                                  : source_of<TH, VEC>(p_h, row, Extent{p.rows, p.ld_h}, cols);
+                                  : source_of<TH, VEC>(p_h, row, p.ld_h, edge, cols);
       const Source s_y = y_kept ? Source{p.y_ckpt + row * p.ck.ld_q + c0, q_bytes}
-                         : has_y ? source_of<TY, VEC>(p_y, row, Extent{p.rows, p.ld_y}, cols) : none;
-      const Source s_g = token ? source_of<TY, VEC>(p_gate, row, Extent{p.rows, p.ld_gate}, cols) : none;
+                         : has_y ? source_of<TY, VEC>(p_y, row, p.ld_y, edge, cols) : none;
+      const Source s_g = token ? source_of<TY, VEC>(p_gate, row, p.ld_gate, edge, cols) : none;
       const uint32_t e = (uint32_t)p.ck.ld_e;
       mbar_arrive_expect_tx(bar, s_dx.bytes + s_dh.bytes + s_h.bytes + s_y.bytes + s_g.bytes + (pre && h_kept ? e : 0) +
                                      (y_kept ? e : 0));
@@ -290,20 +294,21 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
       r_pre = factors[g][0][f];
       r_post = factors[g][1][f];
       // a copy that never arrives shows as NaN in the row and in the column sums
+      const bool edge = edge_of(row);
       there = there && mbar_poll(&full[stage], phase, nullptr, nullptr, kTimeoutClocks);
       d.fill(0.f);
       if (in) {
-        if (has_dh_in) d = take<TH, VEC>(st + lay.at.dh, p_dh, row, Extent{p.rows, p.ld_dh_in}, 0, t, n, cols);
+        if (has_dh_in) d = take<TH, VEC>(st + lay.at.dh, p_dh, row, p.ld_dh_in, edge, 0, t, n, cols);
         if (!there) d.fill(__uint_as_float(0x7FC00000u));
         if (pre) {
           if (h_kept) {
             hv = take_kept(st + lay.at.h, st + lay.at.h_e + c0 / kActBlock, r_pre, 0, t, n);
           } else {
-            hv = take<TH, VEC>(st + lay.at.h, p_h, row, Extent{p.rows, p.ld_h}, 0, t, n, cols);
+            hv = take<TH, VEC>(st + lay.at.h, p_h, row, p.ld_h, edge, 0, t, n, cols);
 #pragma unroll
             for (int j = 0; j < 4; ++j) hv.p[j] = mul2(hv.p[j], both(r_pre));
           }
-          F8 dx = take<TY, VEC>(st + lay.at.dx, p_dx, row, Extent{p.rows, p.ld_dx}, 0, t, n, cols);
+          F8 dx = take<TY, VEC>(st + lay.at.dx, p_dx, row, p.ld_dx, edge, 0, t, n, cols);
 #pragma unroll
           for (int j = 0; j < 4; ++j) a_pre.p[j] = fma2(dx.p[j], hv.p[j], a_pre.p[j]);
           if (w_pre) {
@@ -322,12 +327,12 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
         if (y_kept) {
           yv = take_kept(st + lay.at.y, st + lay.at.y_e + c0 / kActBlock, post ? r_post : 1.f, 0, t, n);
         } else if (has_y) {
-          yv = take<TY, VEC>(st + lay.at.y, p_y, row, Extent{p.rows, p.ld_y}, 0, t, n, cols);
+          yv = take<TY, VEC>(st + lay.at.y, p_y, row, p.ld_y, edge, 0, t, n, cols);
           if (post)
 #pragma unroll
             for (int j = 0; j < 4; ++j) yv.p[j] = mul2(yv.p[j], both(r_post));
         }
-        if (token) gv = take<TY, VEC>(st + lay.at.gate, p_gate, row, Extent{p.rows, p.ld_gate}, 0, t, n, cols);
+        if (token) gv = take<TY, VEC>(st + lay.at.gate, p_gate, row, p.ld_gate, edge, 0, t, n, cols);
       }
     }
     // behind this barrier every thread has read this row

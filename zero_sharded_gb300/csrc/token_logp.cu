@@ -16,7 +16,10 @@
 // key find them instead.
 //
 // Backward is elementwise: p = exp(z - lse).  Bound by memory both ways: s bytes an
-// element forward, 2 s backward.
+// element forward, 2 s backward.  Measured: 8191 x 131072 bf16 310 us (1.02 of the copy rate) without alternatives,
+// 392 with 8, 469 with 20: the search for them holds a block up for about 6 us a row.  Four blocks of 256 threads
+// an SM cover each other's searches best (eight of 128: 448 us with 8, two of 512: 424).  Backward 8192 x 100003 bf16
+// 529 us, 0.91 of the copy rate.
 
 #include <cuda_runtime.h>
 
