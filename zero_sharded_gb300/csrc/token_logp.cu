@@ -8,18 +8,17 @@
 // is 0, so that a masked entry's 2^d d is 0 and not NaN.  Maxima of bf16 are taken before unpacking and
 // the rest runs on pairs: five instructions an element, where memory leaves time for eight.
 //
-// Top alternatives cost no second pass: the k-th largest of the maxima of groups of 4 to 16
-// threads (disjoint parts of the row) is a bound that the k largest elements reach, so only the parts of threads
-// whose own maximum reaches it are read again, by the whole block at once.  Keys of (value,
-// complement of the index) make the order total.  Should ties or a skewed row
-// put forward more than the buffer holds, k rounds of a block-wide maximum below the last
-// key find them instead.
+// Top alternatives cost no second pass: the k-th largest of the maxima of groups of 4
+// threads (disjoint parts of the row) is a bound that the k largest elements reach.  Threads keep the maxima of 16 stretches
+// of their vectors, and only the stretches that reach the bound are read again, by the whole block at once (whole threads'
+// parts read again: 392 us at 8191 x 131072 with 8 alternatives).  Keys of (value, complement of the index) make the
+// order total.  Should ties or a skewed row put forward more than the buffers hold, k rounds of a block-wide maximum
+// below the last key find them instead.
 //
 // Backward is elementwise: p = exp(z - lse).  Bound by memory both ways: s bytes an
-// element forward, 2 s backward.  Measured: 8191 x 131072 bf16 310 us (1.02 of the copy rate) without alternatives,
-// 392 with 8, 469 with 20: the search for them holds a block up for about 6 us a row.  Four blocks of 256 threads
-// an SM cover each other's searches best (eight of 128: 448 us with 8, two of 512: 424).  Backward 8192 x 100003 bf16
-// 529 us, 0.91 of the copy rate.
+// element forward, 2 s backward.  Measured: 8191 x 131072 bf16 317 us (the copy rate) without alternatives, 351 with 8,
+// 363 with 20.  Four blocks of 256 threads an SM cover each other's searches best (eight of 128 or two of 512 are slower
+// by 8 to 15 %).  Backward 8192 x 100003 bf16 529 us, 0.91 of the copy rate.
 
 #include <cuda_runtime.h>
 
@@ -31,9 +30,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroups = kThreads / 4;     // groups of 4 threads (of 8 or 16 for few alternatives)
-static_assert(kGroups == 64, "two groups a lane");
+constexpr int kGroups = kThreads / 4;     // groups of 4 threads
 constexpr int kCand = 1024;               // candidates that the buffer holds
+constexpr int kUnroll = 4;                // vectors of a thread in flight
+constexpr int kSlots = 16;                // stretches of a thread's vectors whose maxima are kept
+constexpr int kParts = 1024;              // stretches that are read again at most
 constexpr float kMasked = -1e37f;         // a largest logit below this: -inf or a type's lowest value throughout
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 static_assert(kGroups >= CZ_LOGP_MAX_TOP, "the bound needs top_k groups");
@@ -168,40 +169,46 @@ struct LogpShared {
   uint64_t cand[kCand];
   uint64_t top[CZ_LOGP_MAX_TOP];
   uint64_t best[kWarps];
-  float group[kGroups];
+  alignas(16) float group[kGroups];
+  float bound;
   Sums warp[kWarps];
   Sums all;
-  uint16_t part[kThreads];
+  float slot[kSlots][kThreads];            // a thread's stretches: it alone writes and reads them
+  uint16_t part[kParts];
   int n_cand, n_part;
 };
 
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 // The k largest keys of this block's part into sh.top, in order (0 past its elements).
-// own_max: the thread's largest element, NaN if it saw one.
+// own_max: the thread's largest element, NaN if it saw one; stretch: its vectors a slot, slots: how many it filled.
 template <typename T>
-__device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool singles, float own_max, int k) {
+__device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool singles, float own_max, int stretch, int slots,
+                          int k) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float g = own_max;
-  const int width = k <= 8 ? 16 : k <= 16 ? 8 : 4, groups = kThreads / width;   // twice as many groups as k at least
-  for (int d = 1; d < width; d <<= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, d));
-  if ((lane & (width - 1)) == 0) sh.group[threadIdx.x / width] = g;
+  g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, 1));
+  g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, 2));
+  if ((lane & 3) == 0) sh.group[threadIdx.x / 4] = g;
   if (threadIdx.x == 0) sh.n_cand = sh.n_part = 0;
   if ((int)threadIdx.x < k) sh.top[threadIdx.x] = 0;
   __syncthreads();
-  // the k-th largest group maximum (every warp for itself)
-  const float ga = lane < groups ? sh.group[lane] : -INFINITY, gb = lane + 32 < groups ? sh.group[lane + 32] : -INFINITY;
-  int ra = 0, rb = 0;
-#pragma unroll 8
-  for (int i = 0; i < groups; ++i) {
-    const float o = sh.group[i];
-    ra += (o > ga || (o == ga && i < lane)) ? 1 : 0;
-    rb += (o > gb || (o == gb && i < lane + 32)) ? 1 : 0;
+  // the k-th largest group maximum
+  bool is_nan = false;
+  if (threadIdx.x < kGroups) {
+    const float own = sh.group[threadIdx.x];
+    is_nan = own != own;
+    int rank = 0;
+#pragma unroll 4
+    for (int i = 0; i < kGroups; i += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(&sh.group[i]);
+      rank += (o.x > own || (o.x == own && i < (int)threadIdx.x)) + (o.y > own || (o.y == own && i + 1 < (int)threadIdx.x)) +
+              (o.z > own || (o.z == own && i + 2 < (int)threadIdx.x)) + (o.w > own || (o.w == own && i + 3 < (int)threadIdx.x));
+    }
+    if (rank == k - 1) sh.bound = own;
   }
-  const bool nan = __any_sync(0xffffffffu, ga != ga || gb != gb);
-  const uint32_t ha = __ballot_sync(0xffffffffu, ra == k - 1 && lane < groups),
-                 hb = __ballot_sync(0xffffffffu, rb == k - 1 && lane + 32 < groups);
-  const float bound = ha ? __shfl_sync(0xffffffffu, ga, __ffs(ha) - 1) : __shfl_sync(0xffffffffu, gb, max(__ffs(hb) - 1, 0));
+  const bool nan = __syncthreads_or(is_nan);
+  const float bound = sh.bound;
   if (!nan) {
     auto put_forward = [&](float x, uint32_t i) {
       if (x >= bound) {
@@ -209,27 +216,25 @@ __device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool 
         if (at < kCand) sh.cand[at] = key_of(x, i);
       }
     };
-    // the parts that reach the bound, read again by the whole block: one trip to memory for all
-    if (own_max >= bound) sh.part[atomicAdd(&sh.n_part, 1)] = (uint16_t)threadIdx.x;
+    // the stretches that reach the bound, read again by the whole block: one trip to memory for all
+    if (own_max >= bound)
+      for (int i = 0; i < slots; ++i)
+        if (sh.slot[i][threadIdx.x] >= bound) {
+          const int at = atomicAdd(&sh.n_part, 1);
+          if (at < kParts) sh.part[at] = (uint16_t)(i * kThreads + threadIdx.x);
+        }
     __syncthreads();
-    const int per = (v1 - v0 + kThreads - 1) / kThreads, total = sh.n_part * per;
-    for (int i0 = threadIdx.x; i0 < total; i0 += 2 * kThreads) {
-      uint4 raw[2];
-      int at[2];
+    const int total = min(sh.n_part, kParts) * stretch;
+    for (int i = threadIdx.x; i < total; i += kThreads) {
+      const int part = i / stretch, from = sh.part[part];
+      const int at = v0 + from % kThreads + (from / kThreads * stretch + i - part * stretch) * kThreads;
+      if (at >= v1) continue;
+      const uint4 raw = __ldg(reinterpret_cast<const uint4*>(r.p + r.head) + at);
+      if (!(Vec<T>::largest(raw) >= bound)) continue;
+      float v[Vec<T>::N];
+      Vec<T>::values(raw, v);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int i = i0 + u * kThreads, part = i / per;
-        at[u] = i < total ? v0 + sh.part[part] + (i - part * per) * kThreads : v1;
-        if (at[u] < v1) raw[u] = __ldg(reinterpret_cast<const uint4*>(r.p + r.head) + at[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (at[u] >= v1 || !(Vec<T>::largest(raw[u]) >= bound)) continue;
-        float v[Vec<T>::N];
-        Vec<T>::values(raw[u], v);
-#pragma unroll
-        for (int j = 0; j < Vec<T>::N; ++j) put_forward(v[j], (uint32_t)(r.head + at[u] * Vec<T>::N + j));
-      }
+      for (int j = 0; j < Vec<T>::N; ++j) put_forward(v[j], (uint32_t)(r.head + at * Vec<T>::N + j));
     }
     if (singles && (int)threadIdx.x < r.singles()) {
       const int at = r.single_at(threadIdx.x);
@@ -237,7 +242,7 @@ __device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool 
     }
     __syncthreads();
     const int n = sh.n_cand;
-    if (n <= kCand) {
+    if (n <= kCand && sh.n_part <= kParts) {
       for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint64_t mine = sh.cand[i];
         int rank = 0;
@@ -292,7 +297,10 @@ __global__ void __launch_bounds__(kThreads, 4) logp_fwd_kernel(const __grid_cons
   const int v0 = min(r.nv, part * per), v1 = min(r.nv, v0 + per);
   const float c = p.inv_temp * kLog2e;
   constexpr int N = Vec<T>::N;
-  constexpr int U = 4;
+  constexpr int U = kUnroll;
+  const int stretch = U * ((per + kSlots * U * kThreads - 1) / (kSlots * U * kThreads));   // vectors of a thread a slot
+  float seen = -INFINITY;
+  int slots = 0, held = 0;
 
   Sums a{-INFINITY, 0.f, 0.f};
   const uint4* body = reinterpret_cast<const uint4*>(r.p + r.head);
@@ -328,6 +336,14 @@ __global__ void __launch_bounds__(kThreads, 4) logp_fwd_kernel(const __grid_cons
     for (int u = 0; u < U; ++u) raw[u] = next[u];
     if (i + U * kThreads < v1) fetch(i + U * kThreads);
     const float m = Vec<T>::largest(Vec<T>::larger(Vec<T>::larger(raw[0], raw[1]), Vec<T>::larger(raw[2], raw[3])));
+    if (p.top_k > 0) {
+      seen = max_nan(seen, m);
+      if ((held += U) == stretch) {
+        sh.slot[slots++][threadIdx.x] = seen;
+        seen = -INFINITY;
+        held = 0;
+      }
+    }
     if (!(m <= a.m)) {                         // grown (or NaN): bring the sums to the new base
       const float nm = max_nan(m, a.m);
       const bool was_large = large;
@@ -357,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 4) logp_fwd_kernel(const __grid_cons
       for (int u = 0; u < U; ++u) add(raw[u], [] { return true; });
     }
   }
+  if (held > 0) sh.slot[slots++][threadIdx.x] = seen;
   if (!large && a.m != -INFINITY) {            // from the base to the maximum itself
     const float d = fmaf(-a.m, c, base), f = exp2_fast(d);
 #pragma unroll
@@ -381,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 4) logp_fwd_kernel(const __grid_cons
     a = (lane & d) ? join(o, a, c) : join(a, o, c);      // the same order in both lanes
   }
   if (lane == 0) sh.warp[warp] = a;
-  if (p.top_k > 0) block_top<T>(sh, r, v0, v1, part == 0, own_max, p.top_k);
+  if (p.top_k > 0) block_top<T>(sh, r, v0, v1, part == 0, own_max, stretch, slots, p.top_k);
   else __syncthreads();
   if (threadIdx.x == 0) {
     a = sh.warp[0];
