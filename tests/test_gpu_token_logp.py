@@ -104,6 +104,40 @@ def test_masked_empty_and_special_rows(vocab, dtype, inv_temp):
     assert bool((d[4] == 0).all())
 
 
+@pytest.mark.parametrize("vocab,dtype,repeat", [(1000, "f32", 110), (1003, "bf16", 110), (20001, "f32", 55), (40000, "bf16", 55)])
+def test_many_rows(vocab, dtype, repeat):
+    """Rows enough for the smaller blocks: plain and special ones, repeated; copies at the same alignment (every eighth has
+    it) give the same bits."""
+    x, t = _logits(23, vocab, 17)
+    x[1] = -float("inf")
+    x[2, 1:] = -float("inf")
+    x[3, ::2] = torch.finfo(TYPES[dtype]).min
+    x[4] = 0.25
+    x[5, vocab // 2] = float("nan")
+    x[6] = torch.arange(vocab) * 2.0 ** -12             # ascending
+    x[7] = torch.floor(torch.arange(vocab) / 512.0)
+    x[8, 3] = float("inf")
+    t[2], t[3], t[9], t[10] = 0, 1, -1, vocab
+    x, t = x.to(TYPES[dtype]).cuda(), t.cuda()
+    for k in (32, 5):
+        _check_forward(x, t, 1.25, k)
+        one = _forward(x.repeat(repeat, 1), t.repeat(repeat), 1.25, k)
+        f = O.logp_fwd(x.double().cpu().numpy(), t.cpu().numpy(), 1.25, k)
+        for name, v in one.items():
+            v = v.view(repeat, 23, -1)
+            bits = v if v.dtype == torch.int64 else v.view(torch.int32)
+            assert bool((bits[8:] == bits[:-8]).all()), name
+        m = np.where(np.isfinite(f["lse"]), np.abs(x.double().nan_to_num(0, 0, -1e300).max(1).values.cpu().numpy()), 0) * 1.25
+        mag = lambda v: 5e-6 * (1 + m + np.where(np.isfinite(v), np.abs(v), 0))  # noqa: E731
+        for c in range(8):
+            own = {name: v[23 * c:23 * c + 23] for name, v in one.items()}
+            for name in ("lse", "logp"):
+                _near(own[name], f[name], mag(f[name]), name)
+            _near(own["entropy"], f["entropy"], 5e-6 * (1 + np.log(vocab)), "entropy")
+            assert np.array_equal(own["ids"].cpu().numpy(), f["ids"])
+            _near(own["top"], f["top"], 5e-6 * (1 + m[:, None] + np.where(np.isfinite(f["top"]), np.abs(f["top"]), 0)), "top")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("at", [3e4, -3e4, 1e30, -1e30, 3e38])
 def test_rows_of_large_values(at, dtype):

@@ -16,9 +16,8 @@
 // below the last key find them instead.
 //
 // Backward is elementwise: p = exp(z - lse).  Bound by memory both ways: s bytes an
-// element forward, 2 s backward.  Measured: 8191 x 131072 bf16 317 us (the copy rate) without alternatives, 351 with 8,
-// 363 with 20.  Four blocks of 256 threads an SM cover each other's searches best (eight of 128 or two of 512 are slower
-// by 8 to 15 %).  Backward 8192 x 100003 bf16 529 us, 0.91 of the copy rate.
+// element forward, 2 s backward.  Measured: 8191 x 131072 bf16 308 us (the copy rate) without alternatives, 333 with 8,
+// 356 with 20.  Backward 8192 x 100003 bf16 529 us, 0.91 of the copy rate.
 
 #include <cuda_runtime.h>
 
@@ -28,16 +27,10 @@
 namespace cz {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kGroups = kThreads / 4;     // groups of 4 threads
-constexpr int kCand = 1024;               // candidates that the buffer holds
 constexpr int kUnroll = 4;                // vectors of a thread in flight
 constexpr int kSlots = 16;                // stretches of a thread's vectors whose maxima are kept
-constexpr int kParts = 1024;              // stretches that are read again at most
 constexpr float kMasked = -1e37f;         // a largest logit below this: -inf or a type's lowest value throughout
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-static_assert(kGroups >= CZ_LOGP_MAX_TOP, "the bound needs top_k groups");
 
 __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
   float r;
@@ -149,11 +142,11 @@ struct Row {
   __device__ int single_at(int i) const { return i < head ? i : tail0 + i - head; }
 };
 
-// Calls f(value, index) on every element of thread t's share of vectors [v0, v1), and on its
-// single element if `singles`.
-template <typename T, typename F>
+// Calls f(value, index) on every element of the thread's share of vectors [v0, v1), and on its single element if
+// `singles`.
+template <int THREADS, typename T, typename F>
 __device__ __forceinline__ void each(const Row<T>& r, int v0, int v1, bool singles, F f) {
-  for (int i = v0 + (int)threadIdx.x; i < v1; i += kThreads) {
+  for (int i = v0 + (int)threadIdx.x; i < v1; i += THREADS) {
     float v[Vec<T>::N];
     Vec<T>::values(__ldg(reinterpret_cast<const uint4*>(r.p + r.head) + i), v);
 #pragma unroll
@@ -165,7 +158,14 @@ __device__ __forceinline__ void each(const Row<T>& r, int v0, int v1, bool singl
   }
 }
 
+template <int THREADS>
 struct LogpShared {
+  static constexpr int kWarps = THREADS / 32;
+  static constexpr int kWidth = THREADS >= 128 ? 4 : 2;      // threads of a group
+  static constexpr int kGroups = THREADS / kWidth;
+  static constexpr int kCand = THREADS >= 256 ? 1024 : 512;  // candidates that the buffer holds
+  static constexpr int kParts = kCand;                       // stretches that are read again at most
+  static_assert(kGroups >= CZ_LOGP_MAX_TOP, "the bound needs top_k groups");
   uint64_t cand[kCand];
   uint64_t top[CZ_LOGP_MAX_TOP];
   uint64_t best[kWarps];
@@ -173,7 +173,7 @@ struct LogpShared {
   float bound;
   Sums warp[kWarps];
   Sums all;
-  float slot[kSlots][kThreads];            // a thread's stretches: it alone writes and reads them
+  float slot[kSlots][THREADS];             // a thread's stretches: it alone writes and reads them
   uint16_t part[kParts];
   int n_cand, n_part;
 };
@@ -182,25 +182,26 @@ __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a >
 
 // The k largest keys of this block's part into sh.top, in order (0 past its elements).
 // own_max: the thread's largest element, NaN if it saw one; stretch: its vectors a slot, slots: how many it filled.
-template <typename T>
-__device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool singles, float own_max, int stretch, int slots,
+template <int THREADS, typename T>
+__device__ void block_top(LogpShared<THREADS>& sh, const Row<T>& r, int v0, int v1, bool singles, float own_max, int stretch, int slots,
                           int k) {
+  using S = LogpShared<THREADS>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float g = own_max;
-  g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, 1));
-  g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, 2));
-  if ((lane & 3) == 0) sh.group[threadIdx.x / 4] = g;
+#pragma unroll
+  for (int d = 1; d < S::kWidth; d <<= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, d));
+  if ((lane & (S::kWidth - 1)) == 0) sh.group[threadIdx.x / S::kWidth] = g;
   if (threadIdx.x == 0) sh.n_cand = sh.n_part = 0;
   if ((int)threadIdx.x < k) sh.top[threadIdx.x] = 0;
   __syncthreads();
   // the k-th largest group maximum
   bool is_nan = false;
-  if (threadIdx.x < kGroups) {
+  if (threadIdx.x < S::kGroups) {
     const float own = sh.group[threadIdx.x];
     is_nan = own != own;
     int rank = 0;
 #pragma unroll 4
-    for (int i = 0; i < kGroups; i += 4) {
+    for (int i = 0; i < S::kGroups; i += 4) {
       const float4 o = *reinterpret_cast<const float4*>(&sh.group[i]);
       rank += (o.x > own || (o.x == own && i < (int)threadIdx.x)) + (o.y > own || (o.y == own && i + 1 < (int)threadIdx.x)) +
               (o.z > own || (o.z == own && i + 2 < (int)threadIdx.x)) + (o.w > own || (o.w == own && i + 3 < (int)threadIdx.x));
@@ -213,7 +214,7 @@ __device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool 
     auto put_forward = [&](float x, uint32_t i) {
       if (x >= bound) {
         const int at = atomicAdd(&sh.n_cand, 1);
-        if (at < kCand) sh.cand[at] = key_of(x, i);
+        if (at < S::kCand) sh.cand[at] = key_of(x, i);
       }
     };
     // the stretches that reach the bound, read again by the whole block: one trip to memory for all
@@ -221,13 +222,13 @@ __device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool 
       for (int i = 0; i < slots; ++i)
         if (sh.slot[i][threadIdx.x] >= bound) {
           const int at = atomicAdd(&sh.n_part, 1);
-          if (at < kParts) sh.part[at] = (uint16_t)(i * kThreads + threadIdx.x);
+          if (at < S::kParts) sh.part[at] = (uint16_t)(i * THREADS + threadIdx.x);
         }
     __syncthreads();
-    const int total = min(sh.n_part, kParts) * stretch;
-    for (int i = threadIdx.x; i < total; i += kThreads) {
+    const int total = min(sh.n_part, S::kParts) * stretch;
+    for (int i = threadIdx.x; i < total; i += THREADS) {
       const int part = i / stretch, from = sh.part[part];
-      const int at = v0 + from % kThreads + (from / kThreads * stretch + i - part * stretch) * kThreads;
+      const int at = v0 + from % THREADS + (from / THREADS * stretch + i - part * stretch) * THREADS;
       if (at >= v1) continue;
       const uint4 raw = __ldg(reinterpret_cast<const uint4*>(r.p + r.head) + at);
       if (!(Vec<T>::largest(raw) >= bound)) continue;
@@ -242,8 +243,8 @@ __device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool 
     }
     __syncthreads();
     const int n = sh.n_cand;
-    if (n <= kCand && sh.n_part <= kParts) {
-      for (int i = threadIdx.x; i < n; i += kThreads) {
+    if (n <= S::kCand && sh.n_part <= S::kParts) {
+      for (int i = threadIdx.x; i < n; i += THREADS) {
         const uint64_t mine = sh.cand[i];
         int rank = 0;
         for (int j = 0; j < n; ++j) rank += sh.cand[j] > mine ? 1 : 0;
@@ -257,7 +258,7 @@ __device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool 
   uint64_t last = ~0ull;
   for (int q = 0; q < k; ++q) {
     uint64_t mine = 0;
-    each(r, v0, v1, singles, [&](float x, uint32_t i) {
+    each<THREADS>(r, v0, v1, singles, [&](float x, uint32_t i) {
       const uint64_t key = key_of(x, i);
       if (key < last) mine = max_u64(mine, key);
     });
@@ -267,7 +268,7 @@ __device__ void block_top(LogpShared& sh, const Row<T>& r, int v0, int v1, bool 
     if (lane == 0) sh.best[warp] = mine;
     __syncthreads();
     mine = 0;
-    for (int i = 0; i < kWarps; ++i) mine = max_u64(mine, sh.best[i]);
+    for (int i = 0; i < S::kWarps; ++i) mine = max_u64(mine, sh.best[i]);
     last = mine;
     if (threadIdx.x == 0) sh.top[q] = mine;
     if (mine == 0) break;                  // fewer elements than k in this part
@@ -286,10 +287,11 @@ struct FwdParams {
   float* top_logp;
 };
 
-// A row is taken by a cluster of blocks (one block when there are enough rows).
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) logp_fwd_kernel(const __grid_constant__ FwdParams p, int parts) {
-  __shared__ LogpShared sh;
+// A row is taken by a cluster of blocks (one block when there are enough rows).  1024 threads an SM leave each 64
+// registers: the vectors in flight.
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logp_fwd_kernel(const __grid_constant__ FwdParams p, int parts) {
+  __shared__ LogpShared<THREADS> sh;
   const int64_t row = blockIdx.x / parts;
   const int part = (int)(blockIdx.x - row * parts);
   const Row<T> r(static_cast<const T*>(p.logits) + row * p.ld, p.vocab);
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 4) logp_fwd_kernel(const __grid_cons
   const float c = p.inv_temp * kLog2e;
   constexpr int N = Vec<T>::N;
   constexpr int U = kUnroll;
-  const int stretch = U * ((per + kSlots * U * kThreads - 1) / (kSlots * U * kThreads));   // vectors of a thread a slot
+  const int stretch = U * ((per + kSlots * U * THREADS - 1) / (kSlots * U * THREADS));   // vectors of a thread a slot
   float seen = -INFINITY;
   int slots = 0, held = 0;
 
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 4) logp_fwd_kernel(const __grid_cons
   auto fetch = [&](int i) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      next[u] = i + u * kThreads < v1 ? ld_stream16(body + i + u * kThreads) : make_uint4(none, none, none, none);
+      next[u] = i + u * THREADS < v1 ? ld_stream16(body + i + u * THREADS) : make_uint4(none, none, none, none);
   };
   auto add = [&](const uint4& raw, auto is_large) {
     float v[N];
@@ -330,11 +332,11 @@ __global__ void __launch_bounds__(kThreads, 4) logp_fwd_kernel(const __grid_cons
     }
   };
   fetch(v0 + (int)threadIdx.x);
-  for (int i = v0 + (int)threadIdx.x; i < v1; i += U * kThreads) {
+  for (int i = v0 + (int)threadIdx.x; i < v1; i += U * THREADS) {
     uint4 raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) raw[u] = next[u];
-    if (i + U * kThreads < v1) fetch(i + U * kThreads);
+    if (i + U * THREADS < v1) fetch(i + U * THREADS);
     const float m = Vec<T>::largest(Vec<T>::larger(Vec<T>::larger(raw[0], raw[1]), Vec<T>::larger(raw[2], raw[3])));
     if (p.top_k > 0) {
       seen = max_nan(seen, m);
@@ -398,11 +400,11 @@ __global__ void __launch_bounds__(kThreads, 4) logp_fwd_kernel(const __grid_cons
     a = (lane & d) ? join(o, a, c) : join(a, o, c);      // the same order in both lanes
   }
   if (lane == 0) sh.warp[warp] = a;
-  if (p.top_k > 0) block_top<T>(sh, r, v0, v1, part == 0, own_max, stretch, slots, p.top_k);
+  if (p.top_k > 0) block_top<THREADS>(sh, r, v0, v1, part == 0, own_max, stretch, slots, p.top_k);
   else __syncthreads();
   if (threadIdx.x == 0) {
     a = sh.warp[0];
-    for (int i = 1; i < kWarps; ++i) a = join(a, sh.warp[i], c);
+    for (int i = 1; i < sh.kWarps; ++i) a = join(a, sh.warp[i], c);
     sh.all = a;
   }
   if (parts > 1) cluster_sync();
@@ -540,9 +542,16 @@ int fwd(const FwdParams& p, int64_t rows, cudaStream_t s) {
   // few rows: up to 8 blocks a row, while each keeps two vectors a thread
   int parts = 1;
   const int64_t vectors = p.vocab / Vec<T>::N;
-  while (parts < 8 && rows * parts < 2 * (int64_t)sm_count() && vectors >= (int64_t)parts * 4 * kThreads) parts *= 2;
+  while (parts < 8 && rows * parts < 2 * (int64_t)sm_count() && vectors >= (int64_t)parts * 4 * 256) parts *= 2;
   if (rows * parts > INT32_MAX) return CZ_ERR_UNSUPPORTED;
-  return launch_kernel(logp_fwd_kernel<T>, dim3((unsigned)(rows * parts)), kThreads, 0, s, parts, p, parts);
+  // More, smaller blocks have more rows in their latencies (first loads, joins, the search) at once, as long as the rows
+  // fill all SMs: 8192 x 5000 bf16 with 256 / 128 / 64 threads 59 / 39 / 27 us, 8192 x 32000 107 / 91 / 87; of long rows a
+  // thread of 64 keeps too much: 8191 x 131072 with 20 alternatives 363 / 356 / 387.
+  int threads = 256;
+  const int least = vectors > 4096 ? 128 : 64;
+  while (parts == 1 && threads > least && rows * threads / 2 >= 1024 * (int64_t)sm_count()) threads /= 2;
+  auto* k = threads == 256 ? logp_fwd_kernel<T, 256> : threads == 128 ? logp_fwd_kernel<T, 128> : logp_fwd_kernel<T, 64>;
+  return launch_kernel(k, dim3((unsigned)(rows * parts)), dim3((unsigned)threads), 0, s, parts, p, parts);
 }
 
 template <typename T>
