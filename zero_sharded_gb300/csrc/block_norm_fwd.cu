@@ -9,7 +9,7 @@
 // Bound by memory: 2 s_h + 2 s_y bytes an element, 33/32 more for every checkpoint.  Blocks walk over rows: the
 // next row's loads are in flight while this one is joined, scaled and stored, and the vectors over the columns
 // stay in shared memory.  Measured: 16384 x 5120 bf16 with a channel gate and x kept, the checkpoint's reading back
-// included, 186 us (floor 149); 8192 x 4096 fp32 with a token gate, the same, 113 (89); rows at any alignment 8192 x 4095
+// included, 187 us (floor 149); 8192 x 4096 fp32 with a token gate, the same, 113 (89); rows at any alignment 8192 x 4095
 // bf16 95 (40).
 
 #include <cuda_runtime.h>
@@ -170,12 +170,15 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const __grid_const
 
 template <typename TH, typename TY, bool VEC, bool FULL>
 int launch_f(const NormParams& p, const FwdVectors& at, cudaStream_t s) {
-  // Registers for 3 x 256, 2 x 320 or one larger block an SM; loads at any alignment take more of them.
+  // Blocks an SM and with them registers a thread: as many as hold a row without spilling, which is more for bf16 (8192 x
+  // 8192 bf16 with two blocks of 512 instead of one 116 -> 96 us, 16384 x 5120 with three of 320 instead of two 198 -> 189,
+  // 8192 x 4096 with four of 256 instead of two 63 -> 54; an fp32 stream loses 4 to 5 % with the third and fourth).
+  constexpr bool kAllBf16 = VEC && sizeof(TY) == 2 && sizeof(TH) == 2, kBf16 = VEC && sizeof(TY) == 2;
   auto* k = p.rows_per_block > 1 ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, false, FULL>
             : p.row_threads * 8 >= p.cols ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, true, FULL>
-            : !VEC && p.row_threads <= 256 ? norm_fwd_kernel<TH, TY, VEC, 2, 256, 2, true, FULL>
-            : p.row_threads <= 320 ? norm_fwd_kernel<TH, TY, VEC, 2, 320, VEC ? 2 : 1, true, FULL>
-            : p.row_threads <= 512 ? norm_fwd_kernel<TH, TY, VEC, 2, 512, 1, true, FULL>
+            : p.row_threads <= 256 ? norm_fwd_kernel<TH, TY, VEC, 2, 256, kAllBf16 ? 4 : VEC ? 3 : 2, true, FULL>
+            : p.row_threads <= 320 ? norm_fwd_kernel<TH, TY, VEC, 2, 320, kAllBf16 ? 3 : VEC ? 2 : 1, true, FULL>
+            : p.row_threads <= 512 ? norm_fwd_kernel<TH, TY, VEC, 2, 512, kBf16 ? 2 : 1, true, FULL>
                                    : norm_fwd_kernel<TH, TY, VEC, 2, 1024, 1, true, FULL>;
   const int threads = p.row_threads * p.rows_per_block, smem = at.floats * 4 + (VEC ? 0 : threads / 32 * 1024);
   const int per_sm = blocks_per_sm(reinterpret_cast<const void*>(k), threads, smem);
