@@ -170,12 +170,13 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const __grid_const
 
 template <typename TH, typename TY, bool VEC, bool FULL>
 int launch_f(const NormParams& p, const FwdVectors& at, cudaStream_t s) {
-  // Blocks an SM and with them registers a thread: as many as hold a row without spilling, which is more for bf16 (8192 x
-  // 8192 bf16 with two blocks of 512 instead of one 116 -> 96 us, 16384 x 5120 with three of 320 instead of two 198 -> 189,
-  // 8192 x 4096 with four of 256 instead of two 63 -> 54; an fp32 stream loses 4 to 5 % with the third and fourth).
+  // Blocks an SM and with them registers a thread: as many as hold a row without spilling, which is more for bf16.  Before,
+  // with 3 of 8 elements a thread, 2 of 16 and 1 above 5120 columns, and now: 32768 x 1024 bf16 62 and 57 us, 16384 x 2048
+  // 56 and 52, 8192 x 4096 63 and 54, 16384 x 5120 with a kept copy 198 and 187, 8192 x 8192 116 and 95.  One block more
+  // of each loses (32768 x 1024 with 5: 65), and so does an fp32 stream with these numbers (by 4 to 5 %).
   constexpr bool kAllBf16 = VEC && sizeof(TY) == 2 && sizeof(TH) == 2, kBf16 = VEC && sizeof(TY) == 2;
-  auto* k = p.rows_per_block > 1 ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, false, FULL>
-            : p.row_threads * 8 >= p.cols ? norm_fwd_kernel<TH, TY, VEC, 1, 256, 3, true, FULL>
+  auto* k = p.rows_per_block > 1 ? norm_fwd_kernel<TH, TY, VEC, 1, 256, kBf16 ? 4 : 3, false, FULL>
+            : p.row_threads * 8 >= p.cols ? norm_fwd_kernel<TH, TY, VEC, 1, 256, kAllBf16 ? 6 : 3, true, FULL>
             : p.row_threads <= 256 ? norm_fwd_kernel<TH, TY, VEC, 2, 256, kAllBf16 ? 4 : VEC ? 3 : 2, true, FULL>
             : p.row_threads <= 320 ? norm_fwd_kernel<TH, TY, VEC, 2, 320, kAllBf16 ? 3 : VEC ? 2 : 1, true, FULL>
             : p.row_threads <= 512 ? norm_fwd_kernel<TH, TY, VEC, 2, 512, kBf16 ? 2 : 1, true, FULL>
